@@ -1,0 +1,107 @@
+// head.cuh -- shared declarations of the embedding-head operators (layer norm, linear,
+// balance loss): element access for the two point types, workspace layouts, launchers.
+#pragma once
+
+#include "fk_common.cuh"
+#include "prep_row.cuh"
+
+namespace fk {
+
+__device__ __forceinline__ float head_load(const float *p) { return *p; }
+__device__ __forceinline__ float head_load(const uint16_t *p) { return bf16_val(*p); }
+__device__ __forceinline__ void head_store(float *p, float v) { *p = v; }
+__device__ __forceinline__ void head_store(uint16_t *p, float v) { *p = bf16_bits(v); }
+
+__device__ __forceinline__ float warp_sum_f(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max_f(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// ----------------------------------------------------------------- layer norm
+struct LayerNormArgs {
+    const void *X, *dY;
+    fk_dtype dtype;
+    int64_t N;
+    int d;
+    const float *gamma, *beta;
+    float eps;
+    void *Y;  // forward: Y; backward: dX (optional)
+    float *mean, *rstd;
+    float *dgamma, *dbeta;  // backward, optional
+    float *part;            // backward: [parts][2][d] partial column sums
+    int64_t parts;
+};
+// Row groups whose column sums of the backward pass are formed apart and then joined in
+// order (the workspace holds two rows of d floats for each).
+int64_t layer_norm_parts(int64_t N, int d);
+cudaError_t launch_layer_norm(const LayerNormArgs &a, cudaStream_t st);
+cudaError_t launch_layer_norm_backward(const LayerNormArgs &a, cudaStream_t st);
+
+// ----------------------------------------------------------------- balance loss
+struct BalanceArgs {
+    const void *S;
+    fk_dtype dtype;
+    int64_t N;
+    int K;
+    const int32_t *labels;
+    int top;
+    const int32_t *counts, *rows;
+    float scale, coef;
+    float *loss;
+    void *dS;  // optional
+    double *part;
+    int64_t parts;
+};
+int64_t balance_parts(int64_t N, int K);
+cudaError_t launch_balance_counts(const int32_t *labels, int64_t N, int top, int K,
+                                  int32_t *counts, int32_t *rows, cudaStream_t st);
+cudaError_t launch_balance_loss(const BalanceArgs &a, cudaStream_t st);
+
+// ----------------------------------------------------------------- linear
+// Forward  Z = X W^T + b, Y = act(Z) + R; backward G = dY act'(Z), dX = G W, dW = G^T X,
+// db = column sums of G.
+struct LinearArgs {
+    fk_dtype dtype;
+    int64_t N;
+    int d, m;
+    const void *X, *W;
+    const float *bias;
+    fk_activation act;
+    const void *R;
+    void *Y, *Z;        // forward outputs (Z optional)
+    const void *dY, *Zin;  // backward inputs
+    void *dX, *dW;      // backward outputs, optional
+    float *db;
+};
+size_t linear_ws_bytes(int64_t N, int d, int m, fk_dtype dtype);
+size_t linear_backward_ws_bytes(int64_t N, int d, int m, fk_dtype dtype);
+cudaError_t launch_linear(const LinearArgs &a, void *ws, cudaStream_t st);
+cudaError_t launch_linear_backward(const LinearArgs &a, void *ws, cudaStream_t st);
+
+// act(z): relu max(z, 0); GELU z Phi(z) with the normal distribution function Phi (the
+// erf form); SiLU z / (1 + exp(-z)).
+__device__ __forceinline__ float act_value(float z, int act) {
+    if (act == FK_ACT_RELU) return z > 0.f ? z : (z == z ? 0.f : z);
+    if (act == FK_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
+    if (act == FK_ACT_SILU) return z / (1.f + expf(-z));
+    return z;
+}
+// act'(z); the slope of relu at 0 is 0.
+__device__ __forceinline__ float act_slope(float z, int act) {
+    if (act == FK_ACT_RELU) return z > 0.f ? 1.f : (z == z ? 0.f : z);
+    if (act == FK_ACT_GELU)
+        return 0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * expf(-0.5f * z * z);
+    if (act == FK_ACT_SILU) {
+        const float s = 1.f / (1.f + expf(-z));
+        return s * (1.f + z * (1.f - s));
+    }
+    return 1.f;
+}
+
+}  // namespace fk

@@ -89,6 +89,19 @@ _sig("fk_ivf_search", [_vp, _i64, _int, _vp, _int, _vp, _vp, _vp, _vp, _vp, _vp,
                        _int, _int, _vp, _vp, _vp, _vp, _sz, ctypes.POINTER(FkSearchTiming),
                        _vp])
 _sig("fk_ivf_radii", [_vp, _int, _vp, _vp, _int, _vp, _vp])
+_sig("fk_layer_norm", [_vp, _int, _i64, _int, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp])
+_sig("fk_layer_norm_backward_workspace_size", [_i64, _int, _int, ctypes.POINTER(_sz)])
+_sig("fk_layer_norm_backward", [_vp, _vp, _int, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _sz, _vp])
+_sig("fk_linear_workspace_size", [_i64, _int, _int, _int, ctypes.POINTER(_sz)])
+_sig("fk_linear_backward_workspace_size", [_i64, _int, _int, _int, ctypes.POINTER(_sz)])
+_sig("fk_linear", [_vp, _int, _i64, _int, _vp, _int, _vp, _int, _vp, _vp, _vp, _vp, _sz, _vp])
+_sig("fk_linear_backward", [_vp, _vp, _int, _i64, _int, _vp, _int, _int, _vp, _vp, _vp, _vp, _vp,
+                            _sz, _vp])
+_sig("fk_balance_counts", [_vp, _i64, _int, _int, _vp, _vp, _vp])
+_sig("fk_balance_workspace_size", [_i64, _int, _int, ctypes.POINTER(_sz)])
+_sig("fk_balance_loss", [_vp, _int, _i64, _int, _vp, _int, _vp, _vp, ctypes.c_float,
+                         ctypes.c_float, _vp, _vp, _vp, _sz, _vp])
 
 EXPORTED = ["fk_status_string", "fk_version", "fk_workspace_size", "fk_normalize_rows",
             "fk_centroid_norms", "fk_assign", "fk_update", "fk_lloyd",
@@ -96,7 +109,11 @@ EXPORTED = ["fk_status_string", "fk_version", "fk_workspace_size", "fk_normalize
             "fk_update_partial", "fk_finalize_shards", "fk_split_points",
             "fk_launch_count", "fk_ivf_lists", "fk_lloyd_streamed",
             "fk_streamed_workspace_size", "fk_ivf_norms", "fk_ivf_search_workspace_size",
-            "fk_ivf_search", "fk_ivf_radii", "fk_assign_split"]
+            "fk_ivf_search", "fk_ivf_radii", "fk_assign_split", "fk_layer_norm",
+            "fk_layer_norm_backward_workspace_size", "fk_layer_norm_backward",
+            "fk_linear_workspace_size", "fk_linear_backward_workspace_size", "fk_linear",
+            "fk_linear_backward", "fk_balance_counts", "fk_balance_workspace_size",
+            "fk_balance_loss"]
 
 # Bytes of the static device array fk_assign_noalloc takes its scratch from.
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -496,6 +513,181 @@ def fk_ivf_radii(C: torch.Tensor, X_lists: torch.Tensor, offsets: torch.Tensor,
                              _dev(out, "out", torch.float32, (nlist,)), _stream(stream)),
            "fk_ivf_radii")
     return out
+
+
+# ------------------------------------------------------------------ the embedding head
+# Layer norm, the matrix product with its epilogue, and the balance loss over cells.  Every
+# tensor must be on the current CUDA device.
+
+_ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+
+
+def _here(*tensors):
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current CUDA device (cuda:{dev}), got "
+                             f"{t.device}")
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _activation(act) -> int:
+    if act not in _ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(_ACTIVATIONS)}, got {act!r}")
+    return _ACTIVATIONS[act]
+
+
+def _sized_workspace(where: str, args, device) -> torch.Tensor:
+    out = _sz(0)
+    _check(getattr(_lib, where)(*args, ctypes.byref(out)), where)
+    return torch.zeros(out.value, dtype=torch.uint8, device=device)
+
+
+def _point_code(dtype) -> int:
+    if dtype == torch.float32:
+        return FK_F32
+    if dtype == torch.bfloat16:
+        return FK_BF16
+    raise TypeError(f"unsupported point dtype {dtype}")
+
+
+def fk_layer_norm(X: torch.Tensor, gamma: torch.Tensor | None, beta: torch.Tensor | None,
+                  Y: torch.Tensor, eps: float = 1e-5, mean: torch.Tensor | None = None,
+                  rstd: torch.Tensor | None = None, stream=None):
+    """Layer norm of the rows of X into Y (which may be X); mean and rstd (fp32 [N],
+    optional) are what fk_layer_norm_backward takes."""
+    N, d = _matrix(X, "X")
+    _check(_lib.fk_layer_norm(_dev(X, "X"), _dtype_code(X), N, d,
+                              _opt(gamma, "gamma", torch.float32, (d,)),
+                              _opt(beta, "beta", torch.float32, (d,)), eps,
+                              _dev(Y, "Y", X.dtype, (N, d)),
+                              _opt(mean, "mean", torch.float32, (N,)),
+                              _opt(rstd, "rstd", torch.float32, (N,)),
+                              (_here(X, gamma, beta, Y, mean, rstd), _stream(stream))[1]),
+           "fk_layer_norm")
+
+
+def layer_norm_backward_workspace(N: int, d: int, dtype=torch.float32, device="cuda"):
+    """A workspace tensor for fk_layer_norm_backward."""
+    return _sized_workspace("fk_layer_norm_backward_workspace_size",
+                            (N, d, _point_code(dtype)), device)
+
+
+def fk_layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tensor | None,
+                           mean: torch.Tensor, rstd: torch.Tensor, dX: torch.Tensor | None,
+                           dgamma: torch.Tensor | None, dbeta: torch.Tensor | None,
+                           ws: torch.Tensor, stream=None):
+    """Gradients of fk_layer_norm: dX (may be dY), dgamma and dbeta (fp32 [d]), each
+    skipped when None."""
+    N, d = _matrix(X, "X")
+    _check(_lib.fk_layer_norm_backward(_dev(dY, "dY", X.dtype, (N, d)), _dev(X, "X"),
+                                       _dtype_code(X), N, d,
+                                       _opt(gamma, "gamma", torch.float32, (d,)),
+                                       _dev(mean, "mean", torch.float32, (N,)),
+                                       _dev(rstd, "rstd", torch.float32, (N,)),
+                                       _opt(dX, "dX", X.dtype, (N, d)),
+                                       _opt(dgamma, "dgamma", torch.float32, (d,)),
+                                       _opt(dbeta, "dbeta", torch.float32, (d,)),
+                                       _dev(ws, "ws", torch.uint8), ws.numel(),
+                                       (_here(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, ws),
+                                        _stream(stream))[1]),
+           "fk_layer_norm_backward")
+
+
+def linear_workspace(N: int, d: int, m: int, dtype=torch.float32, device="cuda"):
+    """A workspace tensor for fk_linear."""
+    return _sized_workspace("fk_linear_workspace_size", (N, d, m, _point_code(dtype)), device)
+
+
+def linear_backward_workspace(N: int, d: int, m: int, dtype=torch.float32, device="cuda"):
+    """A workspace tensor for fk_linear_backward."""
+    return _sized_workspace("fk_linear_backward_workspace_size",
+                            (N, d, m, _point_code(dtype)), device)
+
+
+def fk_linear(X: torch.Tensor, W: torch.Tensor, Y: torch.Tensor, ws: torch.Tensor,
+              bias: torch.Tensor | None = None, act: str = "none",
+              residual: torch.Tensor | None = None, Z: torch.Tensor | None = None,
+              stream=None):
+    """Y = act(X W^T + bias) + residual; X [N, d], W [m, d], Y [N, m] (may be residual); Z
+    (optional) receives the pre-activation for fk_linear_backward.  act: "none", "relu",
+    "gelu" or "silu"."""
+    N, d = _matrix(X, "X")
+    m = _matrix(W, "W")[0]
+    _check(_lib.fk_linear(_dev(X, "X"), _dtype_code(X), N, d, _dev(W, "W", X.dtype, (m, d)), m,
+                          _opt(bias, "bias", torch.float32, (m,)), _activation(act),
+                          _opt(residual, "residual", X.dtype, (N, m)),
+                          _dev(Y, "Y", X.dtype, (N, m)), _opt(Z, "Z", X.dtype, (N, m)),
+                          _dev(ws, "ws", torch.uint8), ws.numel(),
+                          (_here(X, W, bias, residual, Y, Z, ws), _stream(stream))[1]),
+           "fk_linear")
+
+
+def fk_linear_backward(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, ws: torch.Tensor,
+                       act: str = "none", Z: torch.Tensor | None = None,
+                       dX: torch.Tensor | None = None, dW: torch.Tensor | None = None,
+                       dbias: torch.Tensor | None = None, stream=None):
+    """Gradients of fk_linear from dY [N, m] and, unless act is "none", the pre-activation
+    Z it returned: dX [N, d], dW [m, d], dbias fp32 [m], each skipped when None."""
+    N, d = _matrix(X, "X")
+    m = _matrix(W, "W")[0]
+    _check(_lib.fk_linear_backward(_dev(dY, "dY", X.dtype, (N, m)), _dev(X, "X"),
+                                   _dtype_code(X), N, d, _dev(W, "W", X.dtype, (m, d)), m,
+                                   _activation(act), _opt(Z, "Z", X.dtype, (N, m)),
+                                   _opt(dX, "dX", X.dtype, (N, d)),
+                                   _opt(dW, "dW", X.dtype, (m, d)),
+                                   _opt(dbias, "dbias", torch.float32, (m,)),
+                                   _dev(ws, "ws", torch.uint8), ws.numel(),
+                                   (_here(dY, X, W, Z, dX, dW, dbias, ws),
+                                    _stream(stream))[1]),
+           "fk_linear_backward")
+
+
+def fk_balance_counts(labels: torch.Tensor, counts: torch.Tensor, rows: torch.Tensor,
+                      stream=None):
+    """counts (int32 [K]) of the cells selected by labels (int32 [N] or [N, top]; entries
+    outside [0, K) select nothing) and rows (int32 [1]), the rows that select any."""
+    N = labels.shape[0]
+    top = labels.shape[1] if labels.dim() == 2 else 1
+    K = counts.shape[0]
+    shape = (N, top) if labels.dim() == 2 else (N,)
+    _check(_lib.fk_balance_counts(_dev(labels, "labels", torch.int32, shape), N, top, K,
+                                  _dev(counts, "counts", torch.int32, (K,)),
+                                  _dev(rows, "rows", torch.int32, (1,)),
+                                  (_here(labels, counts, rows), _stream(stream))[1]),
+           "fk_balance_counts")
+
+
+def balance_workspace(N: int, K: int, dtype=torch.float32, device="cuda"):
+    """A workspace tensor for fk_balance_loss."""
+    return _sized_workspace("fk_balance_workspace_size", (N, K, _point_code(dtype)), device)
+
+
+def fk_balance_loss(S: torch.Tensor, labels: torch.Tensor, counts: torch.Tensor,
+                    rows: torch.Tensor, loss: torch.Tensor, dS: torch.Tensor | None,
+                    ws: torch.Tensor, scale: float = 1.0, coef: float = 1.0, stream=None):
+    """Balance loss (fp32 [1]) of the scores S [N, K] and its gradient dS (may be S; None
+    skips it), with the counts and rows of fk_balance_counts."""
+    N, K = _matrix(S, "S")
+    top = labels.shape[1] if labels.dim() == 2 else 1
+    shape = (N, top) if labels.dim() == 2 else (N,)
+    _check(_lib.fk_balance_loss(_dev(S, "S"), _dtype_code(S), N, K,
+                                _dev(labels, "labels", torch.int32, shape), top,
+                                _dev(counts, "counts", torch.int32, (K,)),
+                                _dev(rows, "rows", torch.int32, (1,)), scale, coef,
+                                _dev(loss, "loss", torch.float32, (1,)),
+                                _opt(dS, "dS", S.dtype, (N, K)),
+                                _dev(ws, "ws", torch.uint8), ws.numel(),
+                                (_here(S, labels, counts, rows, loss, dS, ws),
+                                 _stream(stream))[1]),
+           "fk_balance_loss")
 
 
 class IvfFlatIndex:

@@ -393,6 +393,104 @@ FK_API fk_status fk_ivf_search(const float *Q, int64_t nq, int d, const float *C
                                int32_t *probes, void *ws, size_t ws_bytes,
                                fk_search_timing *timing, fk_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------
+ * The embedding head: the operators that turn a model's hidden states into points and
+ * queries, in both directions, and the loss that keeps the cells of a clustering even.  The
+ * source pages name such uses (the Flash-KMeans article lists clustering inside models, MoE
+ * routing among it) and define none of these operators; the formulas here do.
+ *
+ * Common to all of them:
+ *   - points and matrices are FK_F32 or FK_BF16, row-major and contiguous; vectors (bias,
+ *     gamma, beta and their gradients, mean, rstd) are fp32, as centroids are;
+ *   - any d, m, K >= 1 and 0 <= N < 2^31, element-aligned pointers (16-byte aligned rows are
+ *     faster); N = 0 writes no row, and gradients that are sums over rows become 0;
+ *   - products, statistics and sums are accumulated in fp32 or more and every output is
+ *     rounded once; no floating-point atomics, so results repeat bit for bit;
+ *   - outputs overlap neither an input nor one another, except where "may be" says so
+ *     (then they start at the same address); NULL skips an optional output;
+ *   - calls are asynchronous on `stream` and can be captured into a CUDA graph (each graph
+ *     that may run beside another needs a workspace of its own). */
+
+/* Row layer norm: mean_i and rstd_i = 1 / sqrt(var_i + eps) of row i (var over the d
+ * columns, divided by d), Y = (X - mean) rstd gamma + beta.  gamma, beta: d floats or NULL
+ * (1 and 0).  mean, rstd: N floats, optional (the backward pass needs them).  Y may be X.
+ * eps >= 0. */
+FK_API fk_status fk_layer_norm(const void *X, fk_dtype dtype, int64_t N, int d,
+                               const float *gamma, const float *beta, float eps, void *Y,
+                               float *mean, float *rstd, fk_stream_t stream);
+
+/* Bytes of workspace fk_layer_norm_backward needs. */
+FK_API fk_status fk_layer_norm_backward_workspace_size(int64_t N, int d, fk_dtype dtype,
+                                                       size_t *bytes);
+
+/* Gradients of fk_layer_norm from dY and the mean and rstd it returned.  With
+ * h = (X - mean) rstd and w = dY gamma:
+ *   dX = rstd (w - mean_j(w) - h mean_j(w h))   (N x d, optional, may be dY)
+ *   dgamma = sum_i dY h, dbeta = sum_i dY       (d floats, optional)
+ * X is the forward pass's input (so that pass cannot have been in place). */
+FK_API fk_status fk_layer_norm_backward(const void *dY, const void *X, fk_dtype dtype,
+                                        int64_t N, int d, const float *gamma,
+                                        const float *mean, const float *rstd, void *dX,
+                                        float *dgamma, float *dbeta, void *ws,
+                                        size_t ws_bytes, fk_stream_t stream);
+
+typedef enum fk_activation {
+    FK_ACT_NONE = 0,
+    FK_ACT_RELU = 1, /* max(z, 0)                                           */
+    FK_ACT_GELU = 2, /* z Phi(z), Phi the normal distribution function      */
+    FK_ACT_SILU = 3  /* z / (1 + exp(-z))                                   */
+} fk_activation;
+
+/* Bytes of workspace fk_linear and fk_linear_backward need. */
+FK_API fk_status fk_linear_workspace_size(int64_t N, int d, int m, fk_dtype dtype,
+                                          size_t *bytes);
+FK_API fk_status fk_linear_backward_workspace_size(int64_t N, int d, int m, fk_dtype dtype,
+                                                   size_t *bytes);
+
+/* Matrix product with its epilogue: Z = X W^T + bias, Y = act(Z) + residual.
+ * X: N x d, W: m x d (one row per output, like centroids), bias: m floats or NULL,
+ * residual: N x m or NULL, Y: N x m (may be residual), Z: N x m, optional: the
+ * pre-activation, which the backward pass needs when act is not FK_ACT_NONE.
+ * With W = C and bias = -||c||^2 / 2 it scores points against every centroid. */
+FK_API fk_status fk_linear(const void *X, fk_dtype dtype, int64_t N, int d, const void *W,
+                           int m, const float *bias, fk_activation act, const void *residual,
+                           void *Y, void *Z, void *ws, size_t ws_bytes, fk_stream_t stream);
+
+/* Gradients of fk_linear: with G = dY act'(Z) (Z the pre-activation it returned; NULL with
+ * FK_ACT_NONE; relu'(0) = 0),
+ *   dX = G W (N x d), dW = G^T X (m x d), dbias = sum_i G (m floats), each optional.
+ * The residual's gradient is dY itself. */
+FK_API fk_status fk_linear_backward(const void *dY, const void *X, fk_dtype dtype, int64_t N,
+                                    int d, const void *W, int m, fk_activation act,
+                                    const void *Z, void *dX, void *dW, float *dbias, void *ws,
+                                    size_t ws_bytes, fk_stream_t stream);
+
+/* Counts of a selection of cells (or experts): labels N x top int32, row i's selected
+ * cells, e.g. fk_assign's labels (top = 1) or fk_ivf_search's probes.  An entry outside
+ * [0, K) selects nothing; a row without any selection is padding.
+ *   counts[k] = selections of cell k (K int32); *rows = rows that are not padding.
+ * N * top < 2^31.  Shards of a data-parallel run add their counts and rows up before
+ * fk_balance_loss. */
+FK_API fk_status fk_balance_counts(const int32_t *labels, int64_t N, int top, int K,
+                                   int32_t *counts, int32_t *rows, fk_stream_t stream);
+
+/* Bytes of workspace fk_balance_loss needs. */
+FK_API fk_status fk_balance_workspace_size(int64_t N, int K, fk_dtype dtype, size_t *bytes);
+
+/* Balance loss of scores S (N x K) and its gradient.  With n = *rows (at least 1),
+ * f_k = counts[k] / (n top), p_i = softmax(scale S_i) and sums over the rows that are not
+ * padding:
+ *   *loss = coef K sum_k f_k (sum_i p_ik / n)         (1 for an even selection, coef 1)
+ *   dS_ij = coef scale (K / n) p_ij (f_j - sum_k f_k p_ik)     (N x K, optional, may be S)
+ * Padding rows' scores are not used and their gradients are 0; a score of -inf has p = 0, and
+ * so has every score of a row of -inf.  counts and rows (device) come from
+ * fk_balance_counts; labels only tell which rows are padding.  With counts and rows of all
+ * shards, the shards' losses add up to the whole. */
+FK_API fk_status fk_balance_loss(const void *S, fk_dtype dtype, int64_t N, int K,
+                                 const int32_t *labels, int top, const int32_t *counts,
+                                 const int32_t *rows, float scale, float coef, float *loss,
+                                 void *dS, void *ws, size_t ws_bytes, fk_stream_t stream);
+
 /* Scratch held by fk_assign_noalloc: one static device array of this many bytes. */
 #define FK_NOALLOC_SCRATCH_BYTES (8u << 20)
 
