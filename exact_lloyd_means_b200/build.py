@@ -7,9 +7,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfk.so")
 SOURCES = ["fk_api.cu", "prep.cu", "assign_sm100.cu", "screen.cu", "sort_csr.cu", "update.cu",
-           "ivf.cu", "ivf_search.cu", "fk_noalloc.cu", "fk_head.cu", "layer_norm.cu", "linear.cu",
+           "ivf.cu", "ivf_search.cu", "fk_noalloc.cu", "fk_head.cu", "layer_norm.cu", "linear.cu", "gemm_sm100.cu",
            "balance.cu"]
-HEADERS = ["fk_common.cuh", "ptx_sm100.cuh", "prep_row.cuh", "head.cuh"]
+HEADERS = ["fk_common.cuh", "ptx_sm100.cuh", "prep_row.cuh", "head.cuh", "gemm.cuh"]
 
 
 def nvcc() -> str:

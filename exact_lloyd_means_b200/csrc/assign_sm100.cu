@@ -1131,6 +1131,8 @@ __global__ void __launch_bounds__(PairCfg<NP, RES, SCR ? 1 : 4>::kThreads, 1)
     }
 }
 
+}  // namespace
+
 PFN_cuTensorMapEncodeTiled_v12000 tmap_encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     if (!fn) {
@@ -1143,6 +1145,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tmap_encode_fn() {
     }
     return fn;
 }
+
+namespace {
 
 // 2-D bf16 tensor map over a row-major [rows][cols] plane with the given row stride,
 // box_cols x box_rows boxes (64 columns = 128 bytes with 128-byte swizzle, or 16 columns =

@@ -1,0 +1,548 @@
+// gemm_sm100.cu -- C = A B^T on the tensor cores, with its epilogue, for fk_linear and its
+// gradients.
+//
+//   * persistent grid; a unit of work is one output tile (128 * CG rows by BN columns) over
+//     one part of the depth.  CG = 2: a cluster of two CTAs, each with 128 rows of A, half
+//     the columns of B and the 128 x 256 accumulator of its rows (cta_group::2, M = 256);
+//   * warp 0: TMA producer, a ring of stages of 64 of the depth; warp 1: tcgen05.mma issuer,
+//     two accumulators in tensor memory, so that a tile's epilogue overlaps the next tile's
+//     products; warps 2..9: epilogue, two groups of four warps, half the columns each.  A
+//     warp takes 32 rows x 32 columns from tensor memory through its own 4 KB of shared
+//     memory (16-byte chunks XORed with the row, no bank conflicts), so that every global
+//     access (residual, pre-activation, output) is 16 bytes a lane along a row;
+//   * either operand may be stored along the depth (K-major) or along its rows (MN-major):
+//     both are 128-byte-swizzled TMA boxes, and the MMA descriptors say which.  So the three
+//     products of a linear layer and its gradients read their operands as they lie;
+//   * fp32 operands come as three bf16 planes (x = x0 + x1 + x2, 8 bits each, exact).  Six
+//     of the nine products keep everything above 2^-24 of the result: the small ones come
+//     first, so that they are added before the accumulator has its full size;
+//   * every wait is bounded; on expiry the CTA records the timeout and winds down.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "gemm.cuh"
+#include "ptx_sm100.cuh"
+
+namespace fk {
+
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encode_fn();  // assign_sm100.cu
+
+namespace {
+
+constexpr int kBandRows = 8;  // tiles of one column band that run side by side
+
+template <int CG, int BN>
+struct GemmCfg {
+    static constexpr int kABytes = kBM * kBK * 2;
+    static constexpr int kBRows = BN / CG;
+    static constexpr int kBBytes = kBRows * kBK * 2;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = CG == 2 ? 6 : (BN == 128 ? 6 : 8);
+    static constexpr int kEpiWarps = 8;
+    static constexpr int kStageOut = 32 * 32 * 4;  // one warp's 32 x 32 fp32
+    static constexpr int kBarBytes = 256;
+    static constexpr int kSmemBytes =
+        kStages * kStageBytes + kEpiWarps * kStageOut + kBarBytes + 1024;
+    static constexpr int kThreads = 64 + kEpiWarps * 32;
+    static constexpr int kTmemCols = 2 * BN;
+    static constexpr int kGroupCols = BN / 2;  // columns of one epilogue group
+    static_assert(kSmemBytes <= 232448, "shared memory");
+    static_assert(kStageBytes % 1024 == 0, "stage bases stay 1024-byte aligned");
+    static_assert(8 * (2 * kStages + 5) + 8 <= kBarBytes, "barriers");
+};
+
+struct GemmShape {
+    int64_t rows, cols;
+    int nkc;      // chunks of 64 in the depth
+    int splits;
+    int terms;    // products per chunk: 1, or 6 of three planes
+    int a_mn, b_mn;
+    int64_t tiles_r, tiles_c, units;
+    int64_t part_ld;
+};
+
+// The plane of A and of B in product t of the six.
+__device__ __forceinline__ int term_a(int terms, int t) {
+    return terms == 1 ? 0 : (0x010210 >> (4 * t)) & 3;  // 0 1 2 0 1 0
+}
+__device__ __forceinline__ int term_b(int terms, int t) {
+    return terms == 1 ? 0 : (0x001012 >> (4 * t)) & 3;  // 2 1 0 1 0 0
+}
+
+// Unit u: its tile (bands of kBandRows row tiles, rows fastest within a band, so that the
+// tiles running side by side share their operands in L2) and its chunks of the depth.
+struct Unit {
+    int64_t tr, tc;
+    int split, k0, k1;
+};
+template <int CG>
+__device__ __forceinline__ Unit unit_of(const GemmShape &s, int64_t u) {
+    Unit r;
+    const int64_t tiles = s.tiles_r * s.tiles_c;
+    r.split = static_cast<int>(u / tiles);
+    const int64_t t = u - r.split * tiles;
+    const int64_t per_band = kBandRows * s.tiles_c;
+    const int64_t band = t / per_band, in = t - band * per_band;
+    const int64_t left = s.tiles_r - band * kBandRows;
+    const int64_t h = left < kBandRows ? left : kBandRows;
+    r.tc = in / h;
+    r.tr = band * kBandRows + (in - r.tc * h);
+    r.k0 = static_cast<int>(static_cast<int64_t>(s.nkc) * r.split / s.splits);
+    r.k1 = static_cast<int>(static_cast<int64_t>(s.nkc) * (r.split + 1) / s.splits);
+    return r;
+}
+
+__device__ __forceinline__ void gemm_timeout(volatile uint32_t *abort_flag, uint32_t *err) {
+    *abort_flag = 1u;
+    err[0] = kErrTimeout;
+}
+
+template <int CG, int BN, typename T>
+__global__ void __launch_bounds__(GemmCfg<CG, BN>::kThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const GemmShape sh, const Epilogue ep, float *__restrict__ part,
+                uint32_t *__restrict__ err, uint64_t wait_ns) {
+    using Cfg = GemmCfg<CG, BN>;
+    constexpr int S = Cfg::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *stage_out = smem + S * Cfg::kStageBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(stage_out + Cfg::kEpiWarps * Cfg::kStageOut);
+    uint64_t *empty = full + S;
+    uint64_t *tfull = empty + S;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *drain = tempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile uint32_t *abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;
+    const int64_t first = blockIdx.x / CG;
+    const int64_t step = gridDim.x / CG;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(&tfull[a], 1);
+            ptx::mbar_init(&tempty[a], CG * Cfg::kEpiWarps);
+        }
+        ptx::mbar_init(drain, 1);
+        *abort_flag = 0u;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tmA);
+        ptx::prefetch_tmap(&tmB);
+    }
+    if (warp == 1) {
+        if constexpr (CG == 2) {
+            ptx::tmem_alloc_pair(tmem_slot, Cfg::kTmemCols);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(tmem_slot, Cfg::kTmemCols);
+            ptx::tmem_relinquish();
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) ptx::cluster_sync();
+    ptx::tc_fence_after();
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            const uint32_t full_c =
+                CG == 2 ? ptx::mapa_shared(ptx::smem_u32(full), 0) : 0u;
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            for (int64_t u = first; u < sh.units && ok; u += step) {
+                const Unit un = unit_of<CG>(sh, u);
+                const int r0 = static_cast<int>(un.tr * (kBM * CG) + rank * kBM);
+                const int c0 = static_cast<int>(un.tc * BN + rank * Cfg::kBRows);
+                for (int t = 0; t < sh.terms && ok; ++t) {
+                    const int pa = term_a(sh.terms, t), pb = term_b(sh.terms, t);
+                    for (int kc = un.k0; kc < un.k1; ++kc) {
+                        if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag, wait_ns)) {
+                            gemm_timeout(abort_flag, err);
+                            ok = false;
+                            break;
+                        }
+                        if (rank == 0)
+                            ptx::mbar_arrive_expect_tx(&full[stage], CG * Cfg::kStageBytes);
+                        uint8_t *sa = smem + stage * Cfg::kStageBytes;
+                        uint8_t *sb = sa + Cfg::kABytes;
+                        const int k = kc * kBK;
+                        auto load = [&](uint8_t *dst, const CUtensorMap *map, int x, int y,
+                                        int p) {
+                            if constexpr (CG == 2)
+                                ptx::tma_load_3d_pair(dst, map, full_c + stage * 8, x, y, p);
+                            else
+                                ptx::tma_load_3d(dst, map, &full[stage], x, y, p);
+                        };
+                        if (sh.a_mn) {
+#pragma unroll
+                            for (int b = 0; b < kBM / 64; ++b)
+                                load(sa + b * 8192, &tmA, r0 + b * 64, k, pa);
+                        } else {
+                            load(sa, &tmA, k, r0, pa);
+                        }
+                        if (sh.b_mn) {
+#pragma unroll
+                            for (int b = 0; b < Cfg::kBRows / 64; ++b)
+                                load(sb + b * 8192, &tmB, c0 + b * 64, k, pb);
+                        } else {
+                            load(sb, &tmB, k, c0, pb);
+                        }
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = ptx::idesc_bf16_f32(kBM * CG, BN) |
+                                   ptx::idesc_mn_major(sh.a_mn != 0, sh.b_mn != 0);
+            const uint64_t ka = sh.a_mn ? 2048 / 16 : 2, kb = sh.b_mn ? 2048 / 16 : 2;
+            uint32_t stage = 0, phase = 0, it = 0;
+            bool ok = true;
+            for (int64_t u = first; u < sh.units && ok; u += step, ++it) {
+                const Unit un = unit_of<CG>(sh, u);
+                const uint32_t acc = it & 1u;
+                if (!ptx::mbar_wait(&tempty[acc], ((it >> 1) & 1u) ^ 1u, abort_flag, wait_ns)) {
+                    gemm_timeout(abort_flag, err);
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t dt = tmem + acc * BN;
+                const int n = sh.terms * (un.k1 - un.k0);
+                for (int i = 0; i < n; ++i) {
+                    if (!ptx::mbar_wait(&full[stage], phase, abort_flag, wait_ns)) {
+                        gemm_timeout(abort_flag, err);
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t sa = ptx::smem_u32(smem + stage * Cfg::kStageBytes);
+                    const uint32_t sb = sa + Cfg::kABytes;
+                    const uint64_t da = sh.a_mn ? ptx::sdesc_mn_sw128(sa)
+                                                : ptx::sdesc_k_sw128(sa);
+                    const uint64_t db = sh.b_mn ? ptx::sdesc_mn_sw128(sb)
+                                                : ptx::sdesc_k_sw128(sb);
+#pragma unroll
+                    for (int ks = 0; ks < kBK / 16; ++ks) {
+                        const uint32_t more = i > 0 || ks > 0 ? 1u : 0u;
+                        if constexpr (CG == 2)
+                            ptx::mma_bf16_ss_pair(dt, da + ks * ka, db + ks * kb, idesc, more);
+                        else
+                            ptx::mma_bf16_ss(dt, da + ks * ka, db + ks * kb, idesc, more);
+                    }
+                    if constexpr (CG == 2)
+                        ptx::mma_commit_pair(&empty[stage], 0x3);
+                    else
+                        ptx::mma_commit(&empty[stage]);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if constexpr (CG == 2)
+                    ptx::mma_commit_pair(&tfull[acc], 0x3);
+                else
+                    ptx::mma_commit(&tfull[acc]);
+            }
+            if (!ok) {
+                if constexpr (CG == 2)
+                    ptx::mma_commit_pair(drain, 0x1);
+                else
+                    ptx::mma_commit(drain);
+                ptx::mbar_wait(drain, 0u, nullptr, wait_ns);
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        constexpr int V = kVec<T>;
+        constexpr int LPR = 32 / V;            // lanes per row of 32 columns
+        constexpr int RPP = 32 / LPR;          // rows per pass
+        const int g = (warp - 2) >> 2;
+        const int q = warp & 3;
+        float4 *st = reinterpret_cast<float4 *>(stage_out + (warp - 2) * Cfg::kStageOut);
+        const uint32_t tempty_c =
+            CG == 2 ? ptx::mapa_shared(ptx::smem_u32(tempty), 0) : 0u;
+        const int lr = lane / LPR, lc = (lane % LPR) * V;
+        uint32_t it = 0;
+        for (int64_t u = first; u < sh.units; u += step, ++it) {
+            const Unit un = unit_of<CG>(sh, u);
+            const uint32_t acc = it & 1u;
+            const int64_t r0 = un.tr * (kBM * CG) + rank * kBM + q * 32;
+            const int64_t c0 = un.tc * BN + g * Cfg::kGroupCols;
+            uint32_t good = 0;
+            if (lane == 0) good = ptx::mbar_wait(&tfull[acc], (it >> 1) & 1u, abort_flag, wait_ns);
+            if (!__shfl_sync(0xffffffffu, good, 0)) {
+                if (lane == 0) gemm_timeout(abort_flag, err);
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN +
+                                g * Cfg::kGroupCols;
+#pragma unroll 1
+            for (int c = 0; c < Cfg::kGroupCols / 32; ++c) {
+                const int64_t col = c0 + c * 32 + lc;
+                const bool in = col < sh.cols;
+                uint4 res[RPP == 8 ? 4 : 8];
+                constexpr int P = 32 / RPP;
+                if (sh.splits == 1) {
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        const int64_t row = r0 + p * RPP + lr;
+                        res[p] = in && row < sh.rows ? epilogue_residual<T>(ep, row, col)
+                                                     : make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                __syncwarp();
+                float v[32];
+                ptx::tmem_ld32_sync(tb + c * 32, v);
+                if (c == Cfg::kGroupCols / 32 - 1) {  // the accumulator is free again
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 2)
+                            ptx::mbar_arrive_cluster(tempty_c + acc * 8);
+                        else
+                            ptx::mbar_arrive(&tempty[acc]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    st[lane * 8 + (j ^ (lane & 7))] =
+                        make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                __syncwarp();
+                if (sh.splits == 1) {
+                    float b[V];
+                    epilogue_bias<T>(ep, col, b);
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        const int lrow = p * RPP + lr;
+                        const int64_t row = r0 + lrow;
+                        float z[V];
+#pragma unroll
+                        for (int j = 0; j < V / 4; ++j) {
+                            const float4 f = st[lrow * 8 + ((lc / 4 + j) ^ (lrow & 7))];
+                            z[4 * j] = f.x;
+                            z[4 * j + 1] = f.y;
+                            z[4 * j + 2] = f.z;
+                            z[4 * j + 3] = f.w;
+                        }
+                        if (in && row < sh.rows) epilogue_store<T>(ep, row, col, z, b, res[p]);
+                    }
+                } else {  // fp32 partial products, four columns a lane
+                    float *dst = part + un.split * sh.rows * sh.part_ld;
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) {
+                        const int lrow = p * 4 + lane / 8;
+                        const int64_t row = r0 + lrow, pc = c0 + c * 32 + (lane & 7) * 4;
+                        if (row < sh.rows && pc < sh.part_ld)
+                            *reinterpret_cast<float4 *>(dst + row * sh.part_ld + pc) =
+                                st[lrow * 8 + ((lane & 7) ^ (lrow & 7))];
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+
+    // ---------------------------------------------------------------- teardown
+    ptx::tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) {
+        __syncwarp();
+        ptx::cluster_sync();
+    }
+    if (*abort_flag) {  // give copies already in flight a moment to land (bounded)
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (ptx::globaltimer_ns() - t0 < 200000ull) {
+        }
+    }
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        if constexpr (CG == 2)
+            ptx::tmem_dealloc_pair(tmem, Cfg::kTmemCols);
+        else
+            ptx::tmem_dealloc(tmem, Cfg::kTmemCols);
+    }
+}
+
+// Join the partial products of a split depth, in order, and apply the epilogue.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    gemm_join_kernel(const float *__restrict__ part, int splits, int64_t rows, int64_t part_ld,
+                     int64_t per_row, const Epilogue ep) {
+    constexpr int V = kVec<T>;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t total = rows * per_row;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < total;
+         t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t row = t / per_row, col = (t - row * per_row) * V;
+        const uint4 r = epilogue_residual<T>(ep, row, col);
+        float b[V], z[V];
+        epilogue_bias<T>(ep, col, b);
+#pragma unroll
+        for (int j = 0; j < V; ++j) z[j] = 0.f;
+        const float *p = part + row * part_ld + col;
+        for (int s = 0; s < splits; ++s) {
+#pragma unroll
+            for (int j = 0; j < V; j += 4) {
+                if (col + j < part_ld) {
+                    const float4 f = *reinterpret_cast<const float4 *>(p + j);
+                    z[j] += f.x;
+                    z[j + 1] += f.y;
+                    z[j + 2] += f.z;
+                    z[j + 3] += f.w;
+                }
+            }
+            p += rows * part_ld;
+        }
+        epilogue_store<T>(ep, row, col, z, b, r);
+    }
+}
+
+// Map of an operand's planes [planes][outer][inner] (rows of ld), boxes of 64 x box_outer.
+bool operand_map(CUtensorMap *m, const GemmOperand &o, int64_t outer, int64_t inner, int planes,
+                 int box_outer) {
+    auto fn = tmap_encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                          static_cast<cuuint64_t>(planes)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.ld) * 2,
+                             static_cast<cuuint64_t>(o.ld) * 2 * static_cast<cuuint64_t>(outer)};
+    cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_outer), 1u};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(o.base), dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int CG, int BN, typename T>
+cudaError_t launch_cfg(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
+    using Cfg = GemmCfg<CG, BN>;
+    auto kernel = gemm_kernel<CG, BN, T>;
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = smem_opt_in(kernel, Cfg::kSmemBytes, smem_set);
+    if (e != cudaSuccess) return e;
+    CUtensorMap tA, tB;
+    const bool ok =
+        (a.A.mn_major ? operand_map(&tA, a.A, a.depth, a.rows, a.planes, 64)
+                      : operand_map(&tA, a.A, a.rows, a.depth, a.planes, kBM)) &&
+        (a.B.mn_major ? operand_map(&tB, a.B, a.depth, a.cols, a.planes, 64)
+                      : operand_map(&tB, a.B, a.cols, a.depth, a.planes, Cfg::kBRows));
+    if (!ok) return cudaErrorInvalidValue;
+    GemmShape s{};
+    s.rows = a.rows;
+    s.cols = a.cols;
+    s.nkc = static_cast<int>(ceil_div(a.depth, kBK));
+    s.splits = p.splits;
+    s.terms = a.planes == 3 ? 6 : 1;
+    s.a_mn = a.A.mn_major;
+    s.b_mn = a.B.mn_major;
+    s.tiles_r = ceil_div(a.rows, kBM * CG);
+    s.tiles_c = ceil_div(a.cols, BN);
+    s.units = s.tiles_r * s.tiles_c * p.splits;
+    s.part_ld = round_up(a.cols, 4);
+    Epilogue ep{};
+    ep.bias = a.bias;
+    ep.R = a.R;
+    ep.C = a.C;
+    ep.Z = a.Z;
+    ep.cols = a.cols;
+    ep.act = a.act;
+    ep.vec = (a.cols * static_cast<int64_t>(sizeof(T))) % 16 == 0 && aligned(a.C, 16) &&
+             aligned(a.Z, 16) && aligned(a.R, 16);
+    const int64_t slots = device_sm_count() / CG;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(CG * (s.units < slots ? s.units : slots)));
+    cfg.blockDim = dim3(Cfg::kThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, tA, tB, s, ep, a.part, a.err, kDefaultWaitNs);
+    if (e != cudaSuccess) return e;
+    note_launch();
+    if (p.splits > 1) {
+        const int64_t work = a.rows * ceil_div(a.cols, kVec<T>);
+        const int64_t g = ceil_div(work, 256), cap = static_cast<int64_t>(device_sm_count()) * 8;
+        e = launch_pdl(gemm_join_kernel<T>, dim3(static_cast<unsigned>(g < cap ? g : cap)),
+                       dim3(256), 0, st, static_cast<const float *>(a.part), p.splits, a.rows,
+                       s.part_ld, ceil_div(a.cols, kVec<T>), ep);
+        if (e == cudaSuccess) note_launch();
+    }
+    return e;
+}
+
+template <typename T>
+cudaError_t launch_t(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
+    if (p.cg == 2) return launch_cfg<2, 256, T>(a, p, st);
+    if (p.bn == 128) return launch_cfg<1, 128, T>(a, p, st);
+    return launch_cfg<1, 64, T>(a, p, st);
+}
+
+}  // namespace
+
+// The cheapest cut by a model in SM cycles: a chunk of 64 of the depth takes the time its
+// operands take to arrive (64 bytes a cycle and SM) or its products, whichever is longer: 512
+// for the pair's 256 x 256 tile, 512 for 128 x 128, 384 for 128 x 64; a unit fills its ring
+// and empties its last accumulator once (about 4000); joining a split depth costs a launch
+// (about 4000) and its traffic (about 3000 bytes a cycle through L2).  A part of the depth
+// keeps at least four chunks.
+GemmPlan gemm_plan(int64_t rows, int64_t cols, int64_t depth, int planes) {
+    const int64_t nkc = ceil_div(depth, kBK);
+    const int terms = planes == 3 ? 6 : 1;
+    static constexpr struct {
+        int cg, bn, cycles;
+    } kCfg[3] = {{2, 256, 512}, {1, 128, 512}, {1, 64, 384}};
+    GemmPlan best{1, 64, 1};
+    double best_cost = -1;
+    for (const auto &c : kCfg) {
+        const int64_t tiles = ceil_div(rows, kBM * c.cg) * ceil_div(cols, c.bn);
+        const int64_t slots = 148 / c.cg;
+        for (int s = 1; s <= 32; ++s) {
+            if (s > 1 && nkc / s < 4) break;
+            const double waves = static_cast<double>(ceil_div(tiles * s, slots));
+            double cost = waves * (static_cast<double>(ceil_div(nkc, s)) * terms * c.cycles) +
+                          4000 + 500 * waves;
+            if (s > 1)
+                cost += 4000 + 8.0 * s * static_cast<double>(rows) * round_up(cols, 4) / 3000;
+            if (best_cost < 0 || cost < best_cost) {
+                best_cost = cost;
+                best = GemmPlan{c.cg, c.bn, s};
+            }
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_gemm(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
+    return a.dtype == FK_F32 ? launch_t<float>(a, p, st) : launch_t<uint16_t>(a, p, st);
+}
+
+}  // namespace fk

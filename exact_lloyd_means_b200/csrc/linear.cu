@@ -1,32 +1,276 @@
 // linear.cu -- Y = act(X W^T + b) + R and its gradients, the embedding head's matrix
 // products: X N x d, W m x d (rows, like centroids), Y N x m.
-#include "head.cuh"
+//
+//   forward   Z = X W^T + b, Y = act(Z) + R          (rows N, columns m, depth d)
+//   backward  G = dY act'(Z), db = column sums of G,
+//             dX = G W (rows N, columns d, depth m), dW = G^T X (rows m, columns d, depth N)
+//
+// The products run in gemm_sm100.cu, which reads an operand along either of its sides, so
+// nothing is transposed.  What this file adds is the staging of operands that TMA cannot
+// read as they lie (fp32 values as three bf16 planes; bf16 rows that are not multiples of 16
+// bytes), G with its column sums, and a kernel for a few rows, which only reads W.
+#include "gemm.cuh"
 
 namespace fk {
 namespace {
 
-// C[i][j] = sum_k A(i, k) B(j, k) over a 64 x 64 tile; A(i, k) = A[i * ar + k * ak] and
-// likewise B, so that the three products of the two passes share one kernel.
-template <typename TA, typename TB, typename TC>
+// ----------------------------------------------------------------- staging
+// The three bf16 pieces of an fp32 value, x = p0 + p1 + p2 (8 significant bits each; each
+// remainder is exact in fp32).  A value that rounds up to infinity is cut instead; an
+// infinity or NaN has no remainder.
+__device__ __forceinline__ void pieces(float x, uint16_t (&p)[3]) {
+    uint32_t h = bf16_bits(x);
+    if ((h & 0x7f80u) == 0x7f80u) {
+        const uint32_t b = __float_as_uint(x);
+        if ((b & 0x7f800000u) == 0x7f800000u) {  // infinity or NaN itself
+            p[0] = static_cast<uint16_t>(h);
+            p[1] = p[2] = 0;
+            return;
+        }
+        h = b >> 16;
+    }
+    const float r = x - bf16_val(static_cast<uint16_t>(h));
+    p[0] = static_cast<uint16_t>(h);
+    p[1] = bf16_bits(r);
+    p[2] = bf16_bits(r - bf16_val(p[1]));
+}
+
+struct StageArgs {
+    const void *src, *Z;  // rows x cols; Z non-null: multiply by act'(Z)
+    int64_t rows;
+    int cols;
+    int act;
+    int vec;         // src and Z in 16-byte vectors
+    uint16_t *out;   // planes [P][rows][ld], or null for column sums alone
+    int64_t ld;
+    float *colpart;  // [parts][cols], or null
+    int tx;          // threads across a row (a power of two up to 32), 8 columns each
+};
+
+// Block (x, y): 8 * tx columns, the y-th of gridDim.y runs of rows.
+template <typename T>
+__global__ void __launch_bounds__(256) stage_kernel(const StageArgs a) {
+    constexpr int P = sizeof(T) == 4 ? 3 : 1;
+    __shared__ float red[256][9];
+    pdl_wait();
+    pdl_trigger();
+    const int tx = threadIdx.x & (a.tx - 1), ty = threadIdx.x / a.tx, nty = 256 / a.tx;
+    const int64_t col = (static_cast<int64_t>(blockIdx.x) * a.tx + tx) * 8;
+    const int64_t i0 = a.rows * blockIdx.y / gridDim.y,
+                  i1 = a.rows * (blockIdx.y + 1) / gridDim.y;
+    const T *src = static_cast<const T *>(a.src), *Z = static_cast<const T *>(a.Z);
+    float sum[8] = {};
+    if (col < a.cols) {
+#pragma unroll 2
+        for (int64_t i = i0 + ty; i < i1; i += nty) {
+            float v[8], z[8];
+            auto load8 = [&](const T *p, float (&o)[8]) {
+                p += i * a.cols + col;
+                if (a.vec) {
+#pragma unroll
+                    for (int h = 0; h < 8 / kVec<T>; ++h) {
+                        float t[kVec<T>];
+                        unpack16(*reinterpret_cast<const uint4 *>(p + h * kVec<T>), t);
+#pragma unroll
+                        for (int j = 0; j < kVec<T>; ++j) o[h * kVec<T> + j] = t[j];
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] = col + j < a.cols ? head_load(p + j) : 0.f;
+                }
+            };
+            load8(src, v);
+            if (Z != nullptr) {
+                load8(Z, z);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= act_slope(z[j], a.act);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += v[j];
+            if (a.out != nullptr) {
+                uint16_t *o = a.out + i * a.ld + col;
+                uint16_t pc[8][3];
+                if constexpr (P == 3) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) pieces(v[j], pc[j]);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) {
+                        uint4 u;
+                        u.x = pc[0][p] | static_cast<uint32_t>(pc[1][p]) << 16;
+                        u.y = pc[2][p] | static_cast<uint32_t>(pc[3][p]) << 16;
+                        u.z = pc[4][p] | static_cast<uint32_t>(pc[5][p]) << 16;
+                        u.w = pc[6][p] | static_cast<uint32_t>(pc[7][p]) << 16;
+                        *reinterpret_cast<uint4 *>(o + p * a.rows * a.ld) = u;
+                    }
+                } else {  // a bf16 operand: G is rounded once
+                    *reinterpret_cast<uint4 *>(o) = pack16(v);
+                }
+            }
+        }
+    }
+    if (a.colpart == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[threadIdx.x][j] = sum[j];
+    __syncthreads();
+    // thread c sums column c of the block over the ty row threads, in order
+    for (int c = threadIdx.x; c < 8 * a.tx; c += 256) {
+        const int64_t cc = static_cast<int64_t>(blockIdx.x) * a.tx * 8 + c;
+        if (cc >= a.cols) continue;
+        float s = 0.f;
+        for (int y = 0; y < nty; ++y) s += red[y * a.tx + c / 8][c % 8];
+        a.colpart[static_cast<int64_t>(blockIdx.y) * a.cols + cc] = s;
+    }
+}
+
+// db = the sum of the parts: 32 columns a block, 8 runs of parts side by side.
 __global__ void __launch_bounds__(256)
-    tile_kernel(const TA *__restrict__ A, int64_t ar, int64_t ak, const TB *__restrict__ B,
-                int64_t br, int64_t bk, int64_t rows, int cols, int64_t depth,
-                const float *__restrict__ bias, int act, const TC *R, TC *C, TC *Z) {
+    col_join_kernel(const float *__restrict__ part, int parts, int cols, float *__restrict__ db) {
+    __shared__ float red[8][33];
+    pdl_wait();
+    pdl_trigger();
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + x;
+    float s = 0.f;
+    if (c < cols)
+        for (int p = y; p < parts; p += 8) s += part[static_cast<int64_t>(p) * cols + c];
+    red[y][x] = s;
+    __syncthreads();
+    if (y == 0 && c < cols) {
+        for (int t = 1; t < 8; ++t) s += red[t][x];
+        db[c] = s;
+    }
+}
+
+int stage_tx(int cols) {
+    int tx = 1;
+    while (tx < 32 && tx * 8 < cols) tx *= 2;
+    return tx;
+}
+
+// Runs of rows the staging kernel is cut into: about six blocks an SM, each thread at
+// least one row.
+int stage_parts(int64_t rows, int cols) {
+    const int tx = stage_tx(cols);
+    const int64_t bx = ceil_div(cols, tx * 8);
+    int64_t p = 148 * 6 / bx;
+    const int64_t most = ceil_div(rows, 256 / tx);
+    if (p > most) p = most;
+    return static_cast<int>(p < 1 ? 1 : p);
+}
+
+template <typename T>
+cudaError_t launch_stage(StageArgs a, cudaStream_t st) {
+    a.tx = stage_tx(a.cols);
+    a.vec = a.cols % 8 == 0 && aligned(a.src, 16) && aligned(a.Z, 16);
+    const dim3 grid(static_cast<unsigned>(ceil_div(a.cols, a.tx * 8)),
+                    static_cast<unsigned>(stage_parts(a.rows, a.cols)));
+    const cudaError_t e = launch_pdl(stage_kernel<T>, grid, dim3(256), 0, st, a);
+    if (e == cudaSuccess) note_launch();
+    return e;
+}
+
+// ----------------------------------------------------------------- a few rows
+// Up to kFewRows rows of X: one warp per output column reads its row of W once and keeps a
+// sum per row of X (which stays in L1).  W is all the traffic.
+constexpr int kFewRows = 8;
+
+template <typename T, int NR>
+__global__ void __launch_bounds__(128)
+    few_rows_kernel(const T *__restrict__ X, const T *__restrict__ W, int N, int d, int vec,
+                    const Epilogue ep) {
+    constexpr int V = kVec<T>;
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    if (c >= ep.cols) return;
+    const T *w = W + c * d;
+    float s[NR] = {};
+    if (vec) {
+#pragma unroll 4
+        for (int k = lane * V; k < d; k += 32 * V) {
+            float a[V];
+            unpack16(*reinterpret_cast<const uint4 *>(w + k), a);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                if (r < N) {
+                    float x[V];
+                    unpack16(*reinterpret_cast<const uint4 *>(X + static_cast<int64_t>(r) * d + k),
+                             x);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) s[r] += a[j] * x[j];
+                }
+            }
+        }
+    } else {
+#pragma unroll 4
+        for (int k = lane; k < d; k += 32) {
+            const float a = head_load(w + k);
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                if (r < N) s[r] += a * head_load(X + static_cast<int64_t>(r) * d + k);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) s[r] = warp_sum_f(s[r]);
+    const float b = ep.bias != nullptr ? ep.bias[c] : 0.f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        if (lane == r && r < N) {
+            const int64_t o = r * ep.cols + c;
+            const float z = __fadd_rn(s[r], b);
+            const float res = ep.R != nullptr ? head_load(static_cast<const T *>(ep.R) + o) : 0.f;
+            if (ep.Z != nullptr) head_store(static_cast<T *>(ep.Z) + o, z);
+            head_store(static_cast<T *>(ep.C) + o, __fadd_rn(act_value(z, ep.act), res));
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_few_rows(const LinearArgs &a, cudaStream_t st) {
+    Epilogue ep{};
+    ep.bias = a.bias;
+    ep.R = a.R;
+    ep.C = a.Y;
+    ep.Z = a.Z;
+    ep.cols = a.m;
+    ep.act = a.act;
+    const int vec = a.d % kVec<T> == 0 && aligned(a.X, 16) && aligned(a.W, 16);
+    const T *X = static_cast<const T *>(a.X), *W = static_cast<const T *>(a.W);
+    const dim3 grid(static_cast<unsigned>(ceil_div(a.m, 4)));
+    const int N = static_cast<int>(a.N);
+    const auto k = N == 1 ? few_rows_kernel<T, 1>
+                          : (N <= 4 ? few_rows_kernel<T, 4> : few_rows_kernel<T, kFewRows>);
+    const cudaError_t e = launch_pdl(k, grid, dim3(128), 0, st, X, W, N, a.d, vec, ep);
+    if (e == cudaSuccess) note_launch();
+    return e;
+}
+
+// ----------------------------------------------------------------- unaligned bf16 operands
+// C[i][j] = sum_k A(i, k) B(j, k) on the CUDA cores, for bf16 operands that start off a
+// 16-byte boundary: any strides, no staging (whose space would be as large as the operand).
+__global__ void __launch_bounds__(256)
+    unaligned_kernel(const uint16_t *__restrict__ A, int64_t ar, int64_t ak,
+                     const uint16_t *__restrict__ B, int64_t br, int64_t bk, int64_t rows,
+                     int64_t depth, const Epilogue ep) {
     __shared__ float sa[16][65], sb[16][65];
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 64;
-    const int c0 = blockIdx.y * 64;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t ct = (ep.cols + 63) / 64;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) / ct * 64;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) % ct * 64;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     float acc[4][4] = {};
     for (int64_t k0 = 0; k0 < depth; k0 += 16) {
         for (int t = threadIdx.x; t < 1024; t += 256) {
             const int k = ak == 1 ? t & 15 : t >> 6, i = ak == 1 ? t >> 4 : t & 63;
             const bool ok = r0 + i < rows && k0 + k < depth;
-            sa[k][i] = ok ? head_load(A + (r0 + i) * ar + (k0 + k) * ak) : 0.f;
+            sa[k][i] = ok ? bf16_val(A[(r0 + i) * ar + (k0 + k) * ak]) : 0.f;
         }
         for (int t = threadIdx.x; t < 1024; t += 256) {
             const int k = bk == 1 ? t & 15 : t >> 6, j = bk == 1 ? t >> 4 : t & 63;
-            const bool ok = c0 + j < cols && k0 + k < depth;
-            sb[k][j] = ok ? head_load(B + (c0 + j) * br + (k0 + k) * bk) : 0.f;
+            const bool ok = c0 + j < ep.cols && k0 + k < depth;
+            sb[k][j] = ok ? bf16_val(B[(c0 + j) * br + (k0 + k) * bk]) : 0.f;
         }
         __syncthreads();
 #pragma unroll
@@ -40,105 +284,200 @@ __global__ void __launch_bounds__(256)
     }
     for (int i = 0; i < 4; ++i)
         for (int j = 0; j < 4; ++j) {
-            const int64_t r = r0 + ty + 16 * i;
-            const int c = c0 + tx + 16 * j;
-            if (r >= rows || c >= cols) continue;
-            const float z = acc[i][j] + (bias ? bias[c] : 0.f);
-            if (Z) head_store(Z + r * cols + c, z);
-            float y = act_value(z, act);
-            if (R) y += head_load(R + r * cols + c);
-            head_store(C + r * cols + c, y);
+            const int64_t r = r0 + ty + 16 * i, c = c0 + tx + 16 * j;
+            if (r >= rows || c >= ep.cols) continue;
+            const int64_t o = r * ep.cols + c;
+            const float z = acc[i][j] + (ep.bias ? ep.bias[c] : 0.f);
+            const float res = ep.R ? bf16_val(static_cast<const uint16_t *>(ep.R)[o]) : 0.f;
+            if (ep.Z) static_cast<uint16_t *>(ep.Z)[o] = bf16_bits(z);
+            static_cast<uint16_t *>(ep.C)[o] = bf16_bits(act_value(z, ep.act) + res);
         }
 }
 
-template <typename T>
-__global__ void slope_kernel(const T *__restrict__ dY, const T *__restrict__ Z, int64_t n,
-                             int act, float *__restrict__ G) {
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const float g = head_load(dY + i);
-        G[i] = act == FK_ACT_NONE ? g : g * act_slope(head_load(Z + i), act);
+// ----------------------------------------------------------------- layouts
+struct LinearLayout {
+    size_t x = 0, w = 0, g = 0, col = 0, part = 0, total = 0;
+    int64_t ldd = 0, ldm = 0;  // staged row lengths
+    int planes = 1;
+    bool stage_x = false, stage_m = false;  // X and W; G and dY
+};
+
+LinearLayout linear_layout(int64_t N, int d, int m, fk_dtype dtype, bool backward) {
+    LinearLayout L;
+    L.planes = dtype == FK_F32 ? 3 : 1;
+    L.ldd = round_up(d, 8);
+    L.ldm = round_up(m, 8);
+    L.stage_x = dtype == FK_F32 || d % 8 != 0;
+    L.stage_m = dtype == FK_F32 || m % 8 != 0;
+    size_t o = 256;  // the error words
+    auto take = [&](int64_t bytes) {
+        const size_t at = o;
+        o += static_cast<size_t>(round_up(bytes, 256));
+        return at;
+    };
+    const bool few = !backward && N <= kFewRows;
+    L.x = take(L.stage_x && !few ? 2 * L.planes * N * L.ldd : 0);
+    L.w = take(L.stage_x && !few ? 2 * L.planes * m * L.ldd : 0);
+    size_t part = 0;
+    if (backward) {
+        L.g = take(2 * L.planes * N * L.ldm);
+        L.col = take(sizeof(float) * static_cast<int64_t>(stage_parts(N, m)) * m);
+        part = gemm_part_bytes(N, d, gemm_plan(N, d, m, L.planes));
+        const size_t q = gemm_part_bytes(m, d, gemm_plan(m, d, N, L.planes));
+        part = part > q ? part : q;
+    } else if (!few) {
+        part = gemm_part_bytes(N, m, gemm_plan(N, m, d, L.planes));
     }
+    L.part = take(static_cast<int64_t>(part));
+    L.total = o;
+    return L;
 }
 
-__global__ void col_sum_kernel(const float *__restrict__ G, int64_t N, int m, int64_t parts,
-                               float *__restrict__ part) {
-    const int j = blockIdx.x * blockDim.x + threadIdx.x;
-    if (j >= m) return;
-    const int64_t p = blockIdx.y;
-    float s = 0.f;
-    for (int64_t i = N * p / parts; i < N * (p + 1) / parts; ++i) s += G[i * m + j];
-    part[p * m + j] = s;
+// An operand of `rows` x `cols` as the tensor cores can read it: staged into `space` where
+// its type or row length asks for it.  `ld` receives its row length.
+template <typename T>
+cudaError_t operand(const void *src, int64_t rows, int cols, bool stage, uint16_t *space,
+                    cudaStream_t st, const uint16_t **base, int64_t *ld) {
+    if (!stage) {
+        *base = static_cast<const uint16_t *>(src);
+        *ld = cols;
+        return cudaSuccess;
+    }
+    *base = space;
+    *ld = round_up(cols, 8);
+    StageArgs s{};
+    s.src = src;
+    s.rows = rows;
+    s.cols = cols;
+    s.out = space;
+    s.ld = *ld;
+    return launch_stage<T>(s, st);
 }
 
-__global__ void col_join_kernel(const float *__restrict__ part, int64_t parts, int m,
-                                float *__restrict__ db) {
-    const int j = blockIdx.x * blockDim.x + threadIdx.x;
-    if (j >= m) return;
-    float s = 0.f;
-    for (int64_t p = 0; p < parts; ++p) s += part[p * m + j];
-    db[j] = s;
+// One product: on the tensor cores, or (bf16 operands off 16-byte boundaries) without them.
+cudaError_t product(const GemmArgs &a, cudaStream_t st) {
+    if (aligned(a.A.base, 16) && aligned(a.B.base, 16))
+        return launch_gemm(a, gemm_plan(a.rows, a.cols, a.depth, a.planes), st);
+    Epilogue ep{};
+    ep.bias = a.bias;
+    ep.R = a.R;
+    ep.C = a.C;
+    ep.Z = a.Z;
+    ep.cols = a.cols;
+    ep.act = a.act;
+    const int64_t tiles = ceil_div(a.rows, 64) * ceil_div(a.cols, 64);
+    if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = launch_pdl(
+        unaligned_kernel, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, st, a.A.base,
+        a.A.mn_major ? 1 : a.A.ld, a.A.mn_major ? a.A.ld : 1, a.B.base,
+        a.B.mn_major ? 1 : a.B.ld, a.B.mn_major ? a.B.ld : 1, a.rows, a.depth, ep);
+    if (e == cudaSuccess) note_launch();
+    return e;
 }
-
-constexpr int64_t kColParts = 128;
 
 template <typename T>
-cudaError_t linear_t(const LinearArgs &a, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>(ceil_div(a.N, 64)),
-                    static_cast<unsigned>(ceil_div(a.m, 64)));
-    tile_kernel<T, T, T><<<grid, 256, 0, st>>>(
-        static_cast<const T *>(a.X), a.d, 1, static_cast<const T *>(a.W), a.d, 1, a.N, a.m, a.d,
-        a.bias, a.act, static_cast<const T *>(a.R), static_cast<T *>(a.Y),
-        static_cast<T *>(a.Z));
-    note_launch();
-    return cudaGetLastError();
+cudaError_t linear_t(const LinearArgs &a, void *ws, cudaStream_t st) {
+    if (a.N <= kFewRows) return launch_few_rows<T>(a, st);
+    const LinearLayout L = linear_layout(a.N, a.d, a.m, a.dtype, false);
+    GemmArgs g{};
+    cudaError_t e = operand<T>(a.X, a.N, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.x), st,
+                               &g.A.base, &g.A.ld);
+    if (e == cudaSuccess)
+        e = operand<T>(a.W, a.m, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.w), st, &g.B.base,
+                       &g.B.ld);
+    if (e != cudaSuccess) return e;
+    g.dtype = a.dtype;
+    g.planes = L.planes;
+    g.rows = a.N;
+    g.cols = a.m;
+    g.depth = a.d;
+    g.bias = a.bias;
+    g.act = a.act;
+    g.R = a.R;
+    g.C = a.Y;
+    g.Z = a.Z;
+    g.part = ws_ptr<float>(ws, L.part);
+    g.err = ws_ptr<uint32_t>(ws, 0);
+    return product(g, st);
 }
 
 template <typename T>
 cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
-    float *G = ws_ptr<float>(ws, 256);
-    float *part = G + a.N * a.m;
-    const T *X = static_cast<const T *>(a.X), *W = static_cast<const T *>(a.W);
-    if (a.N > 0) {
-        slope_kernel<T><<<148 * 8, 256, 0, st>>>(static_cast<const T *>(a.dY),
-                                                 static_cast<const T *>(a.Zin), a.N * a.m, a.act,
-                                                 G);
-        note_launch();
+    const LinearLayout L = linear_layout(a.N, a.d, a.m, a.dtype, true);
+    if (a.N == 0) {
+        cudaError_t e = cudaSuccess;
+        if (a.dW) e = cudaMemsetAsync(a.dW, 0, sizeof(T) * a.m * static_cast<int64_t>(a.d), st);
+        if (e == cudaSuccess && a.db) e = cudaMemsetAsync(a.db, 0, sizeof(float) * a.m, st);
+        return e;
+    }
+    // G, and its column sums from the values before they are rounded to an operand
+    GemmOperand G{};
+    cudaError_t e = cudaSuccess;
+    const bool products = a.dX != nullptr || a.dW != nullptr;
+    const bool write = products && (L.stage_m || a.act != FK_ACT_NONE);
+    if (write || a.db) {
+        StageArgs s{};
+        s.src = a.dY;
+        s.Z = a.act != FK_ACT_NONE ? a.Zin : nullptr;
+        s.rows = a.N;
+        s.cols = a.m;
+        s.act = a.act;
+        s.out = write ? ws_ptr<uint16_t>(ws, L.g) : nullptr;
+        s.ld = L.ldm;
+        s.colpart = a.db ? ws_ptr<float>(ws, L.col) : nullptr;
+        if ((e = launch_stage<T>(s, st)) != cudaSuccess) return e;
     }
     if (a.db) {
-        const unsigned bx = static_cast<unsigned>(ceil_div(a.m, 128));
-        col_sum_kernel<<<dim3(bx, kColParts), 128, 0, st>>>(G, a.N, a.m, kColParts, part);
-        col_join_kernel<<<bx, 128, 0, st>>>(part, kColParts, a.m, a.db);
-        note_launch(2);
-    }
-    if (a.dX && a.N > 0) {
-        const dim3 grid(static_cast<unsigned>(ceil_div(a.N, 64)),
-                        static_cast<unsigned>(ceil_div(a.d, 64)));
-        tile_kernel<float, T, T><<<grid, 256, 0, st>>>(G, a.m, 1, W, 1, a.d, a.N, a.d, a.m,
-                                                       nullptr, FK_ACT_NONE, nullptr,
-                                                       static_cast<T *>(a.dX), nullptr);
+        e = launch_pdl(col_join_kernel, dim3(static_cast<unsigned>(ceil_div(a.m, 32))), dim3(256),
+                       0, st, ws_ptr<const float>(ws, L.col), stage_parts(a.N, a.m), a.m, a.db);
+        if (e != cudaSuccess) return e;
         note_launch();
+    }
+    if (!products) return e;
+    G.base = write ? ws_ptr<uint16_t>(ws, L.g) : static_cast<const uint16_t *>(a.dY);
+    G.ld = write ? L.ldm : a.m;
+    GemmArgs g{};
+    g.dtype = a.dtype;
+    g.planes = L.planes;
+    g.act = FK_ACT_NONE;
+    g.cols = a.d;
+    g.part = ws_ptr<float>(ws, L.part);
+    g.err = ws_ptr<uint32_t>(ws, 0);
+    g.B.mn_major = true;
+    if (a.dX) {
+        g.A = G;
+        e = operand<T>(a.W, a.m, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.w), st, &g.B.base,
+                       &g.B.ld);
+        g.rows = a.N;
+        g.depth = a.m;
+        g.C = a.dX;
+        if (e == cudaSuccess) e = product(g, st);
+        if (e != cudaSuccess) return e;
     }
     if (a.dW) {
-        const dim3 grid(static_cast<unsigned>(ceil_div(a.m, 64)),
-                        static_cast<unsigned>(ceil_div(a.d, 64)));
-        tile_kernel<float, T, T><<<grid, 256, 0, st>>>(G, 1, a.m, X, 1, a.d, a.m, a.d, a.N,
-                                                       nullptr, FK_ACT_NONE, nullptr,
-                                                       static_cast<T *>(a.dW), nullptr);
-        note_launch();
+        g.A = G;
+        g.A.mn_major = true;
+        e = operand<T>(a.X, a.N, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.x), st, &g.B.base,
+                       &g.B.ld);
+        g.rows = a.m;
+        g.depth = a.N;
+        g.C = a.dW;
+        if (e == cudaSuccess) e = product(g, st);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace
 
-size_t linear_ws_bytes(int64_t, int, int, fk_dtype) { return 256; }
-size_t linear_backward_ws_bytes(int64_t N, int, int m, fk_dtype) {
-    return 256 + 4 * (static_cast<size_t>(N) * m + static_cast<size_t>(kColParts) * m);
+size_t linear_ws_bytes(int64_t N, int d, int m, fk_dtype dtype) {
+    return linear_layout(N, d, m, dtype, false).total;
+}
+size_t linear_backward_ws_bytes(int64_t N, int d, int m, fk_dtype dtype) {
+    return linear_layout(N, d, m, dtype, true).total;
 }
 
-cudaError_t launch_linear(const LinearArgs &a, void *, cudaStream_t st) {
-    return a.dtype == FK_F32 ? linear_t<float>(a, st) : linear_t<uint16_t>(a, st);
+cudaError_t launch_linear(const LinearArgs &a, void *ws, cudaStream_t st) {
+    return a.dtype == FK_F32 ? linear_t<float>(a, ws, st) : linear_t<uint16_t>(a, ws, st);
 }
 
 cudaError_t launch_linear_backward(const LinearArgs &a, void *ws, cudaStream_t st) {

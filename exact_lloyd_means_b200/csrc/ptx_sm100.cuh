@@ -164,6 +164,25 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m
         : "memory");
 }
 
+// The same two for 3-D maps (a stack of equal 2-D planes, c2 the plane).
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                            int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map,
+                                                 uint32_t bar_cluster, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
 // ---------------------------------------------------------------- tcgen05 / TMEM
 
 // Allocate `ncols` tensor-memory columns (power of two >= 32); the TMEM address is
@@ -227,6 +246,20 @@ __device__ __forceinline__ uint64_t sdesc_k_sw128(uint32_t saddr) {
     return d;
 }
 
+// Descriptor for a tile whose M (or N) extent is contiguous ("MN-major"), written by TMA with
+// 128-byte swizzle as boxes of 64 such elements (one 128-byte row per k) by 64 k: groups of 8
+// k are 1024 bytes apart (stride byte offset), boxes of 64 elements 8192 bytes apart
+// (leading byte offset); a step of 16 k is 2048 bytes.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(8192u >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
 // Descriptor for a K-major tile with 32-byte swizzle: rows of 32 bytes (16 bf16, one
 // K = 16 MMA step), groups of 8 rows 256 bytes apart (stride byte offset 256), layout
 // type 6 = 32-byte swizzle.  Tile bases are 1024-byte aligned (base offset 0).
@@ -246,6 +279,11 @@ __device__ __forceinline__ uint64_t sdesc_k_sw32(uint32_t saddr) {
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
            (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// The bits of the instruction descriptor that say A (bit 15) or B (bit 16) is MN-major.
+__host__ __device__ constexpr uint32_t idesc_mn_major(bool a, bool b) {
+    return (a ? 1u << 15 : 0u) | (b ? 1u << 16 : 0u);
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T, one M x N x 16 bf16 step, issued by one thread.
