@@ -42,37 +42,6 @@ inline size_t gemm_part_bytes(int64_t rows, int64_t cols, const GemmPlan &p) {
 cudaError_t launch_gemm(const GemmArgs &a, const GemmPlan &p, cudaStream_t st);
 
 // ----------------------------------------------------------------- epilogue
-// V consecutive columns of one row: 16 bytes of the output type.
-template <typename T>
-constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-
-__device__ __forceinline__ void unpack16(const uint4 &u, float (&v)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void unpack16(const uint4 &u, float (&v)[4]) {
-    v[0] = __uint_as_float(u.x);
-    v[1] = __uint_as_float(u.y);
-    v[2] = __uint_as_float(u.z);
-    v[3] = __uint_as_float(u.w);
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&p);
-}
-__device__ __forceinline__ uint4 pack16(const float (&v)[8]) {
-    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                      pack_bf16(v[6], v[7]));
-}
-__device__ __forceinline__ uint4 pack16(const float (&v)[4]) {
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                      __float_as_uint(v[3]));
-}
-
 template <int V>
 __device__ __forceinline__ void act_values(float (&z)[V], int act) {
     if (act == FK_ACT_NONE) return;

@@ -12,6 +12,38 @@ __device__ __forceinline__ float head_load(const uint16_t *p) { return bf16_val(
 __device__ __forceinline__ void head_store(float *p, float v) { *p = v; }
 __device__ __forceinline__ void head_store(uint16_t *p, float v) { *p = bf16_bits(v); }
 
+// ----------------------------------------------------------------- 16-byte vectors
+// Elements of 16 bytes of a point type.
+template <typename T>
+constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+
+__device__ __forceinline__ void unpack16(const uint4 &u, float (&v)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack16(const uint4 &u, float (&v)[4]) {
+    v[0] = __uint_as_float(u.x);
+    v[1] = __uint_as_float(u.y);
+    v[2] = __uint_as_float(u.z);
+    v[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+__device__ __forceinline__ uint4 pack16(const float (&v)[8]) {
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                      pack_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ uint4 pack16(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+}
+
 __device__ __forceinline__ float warp_sum_f(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -21,6 +53,49 @@ __device__ __forceinline__ float warp_max_f(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
+}
+
+// N consecutive elements as they lie in memory: 16 bytes, or one element where rows are not
+// multiples of 16 bytes.
+template <typename T, int N>
+struct Raw;
+template <typename T>
+struct Raw<T, kVec<T>> {
+    uint4 u;
+    __device__ __forceinline__ void load(const T *p) { u = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void get(float (&v)[kVec<T>]) const { unpack16(u, v); }
+    static __device__ __forceinline__ void put(T *p, const float (&v)[kVec<T>]) {
+        *reinterpret_cast<uint4 *>(p) = pack16(v);
+    }
+};
+template <typename T>
+struct Raw<T, 1> {
+    T u;
+    __device__ __forceinline__ void load(const T *p) { u = *p; }
+    __device__ __forceinline__ void zero() { u = T(0); }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = head_load(&u); }
+    static __device__ __forceinline__ void put(T *p, const float (&v)[1]) { head_store(p, v[0]); }
+};
+
+// V fp32 parameters (any 4-byte alignment; `vec`: 16-byte aligned).
+template <int V>
+__device__ __forceinline__ void load_params(const float *p, int vec, float (&v)[V]) {
+    if constexpr (V % 4 == 0) {
+        if (vec) {
+#pragma unroll
+            for (int j = 0; j < V; j += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(p + j);
+                v[j] = f.x;
+                v[j + 1] = f.y;
+                v[j + 2] = f.z;
+                v[j + 3] = f.w;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = p[j];
 }
 
 // ----------------------------------------------------------------- layer norm

@@ -178,8 +178,8 @@ def _opt(t, name, dtype=None, shape=None):
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without making a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -517,45 +517,68 @@ def fk_ivf_radii(C: torch.Tensor, X_lists: torch.Tensor, offsets: torch.Tensor,
 
 # ------------------------------------------------------------------ the embedding head
 # Layer norm, the matrix product with its epilogue, and the balance loss over cells.  Every
-# tensor must be on the current CUDA device.
+# tensor must be on the current CUDA device.  These calls can be as short as a kernel launch,
+# so their checks take one comparison each and look for the reason only when one fails.
 
 _ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+_POINT_CODES = {torch.float32: FK_F32, torch.bfloat16: FK_BF16}
+_f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
 
 
-def _here(*tensors):
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensors must be on the current CUDA device (cuda:{dev}), got "
-                             f"{t.device}")
-
-
-def _matrix(t: torch.Tensor, name: str):
+def _home(t: torch.Tensor, name: str, dims: int = 2) -> int:
+    """The device index of a call's first tensor, which must have `dims` dimensions and be on
+    the current CUDA device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    return t.shape
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _ptr(t, name: str, dtype, shape, dev: int) -> int:
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
+    _dev(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
+def _ptr_or_none(t, name: str, dtype, shape, dev: int):
+    return None if t is None else _ptr(t, name, dtype, shape, dev)
+
+
+def _space(ws, dev: int) -> int:
+    if (isinstance(ws, torch.Tensor) and ws.dtype is _u8 and ws.get_device() == dev
+            and ws.is_contiguous()):
+        return ws.data_ptr()
+    _dev(ws, "ws", _u8)
+    raise ValueError(f"ws must be on cuda:{dev}, got {ws.device}")
+
+
+def _point_code(dtype) -> int:
+    code = _POINT_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported point dtype {dtype}")
+    return code
 
 
 def _activation(act) -> int:
-    if act not in _ACTIVATIONS:
+    code = _ACTIVATIONS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(_ACTIVATIONS)}, got {act!r}")
-    return _ACTIVATIONS[act]
+    return code
 
 
 def _sized_workspace(where: str, args, device) -> torch.Tensor:
     out = _sz(0)
     _check(getattr(_lib, where)(*args, ctypes.byref(out)), where)
-    return torch.zeros(out.value, dtype=torch.uint8, device=device)
-
-
-def _point_code(dtype) -> int:
-    if dtype == torch.float32:
-        return FK_F32
-    if dtype == torch.bfloat16:
-        return FK_BF16
-    raise TypeError(f"unsupported point dtype {dtype}")
+    return torch.zeros(out.value, dtype=_u8, device=device)
 
 
 def fk_layer_norm(X: torch.Tensor, gamma: torch.Tensor | None, beta: torch.Tensor | None,
@@ -563,15 +586,16 @@ def fk_layer_norm(X: torch.Tensor, gamma: torch.Tensor | None, beta: torch.Tenso
                   rstd: torch.Tensor | None = None, stream=None):
     """Layer norm of the rows of X into Y (which may be X); mean and rstd (fp32 [N],
     optional) are what fk_layer_norm_backward takes."""
-    N, d = _matrix(X, "X")
-    _check(_lib.fk_layer_norm(_dev(X, "X"), _dtype_code(X), N, d,
-                              _opt(gamma, "gamma", torch.float32, (d,)),
-                              _opt(beta, "beta", torch.float32, (d,)), eps,
-                              _dev(Y, "Y", X.dtype, (N, d)),
-                              _opt(mean, "mean", torch.float32, (N,)),
-                              _opt(rstd, "rstd", torch.float32, (N,)),
-                              (_here(X, gamma, beta, Y, mean, rstd), _stream(stream))[1]),
-           "fk_layer_norm")
+    dev = _home(X, "X")
+    N, d = shape = X.shape
+    t = X.dtype
+    s = _lib.fk_layer_norm(_ptr(X, "X", t, shape, dev), _point_code(t), N, d,
+                           _ptr_or_none(gamma, "gamma", _f32, (d,), dev),
+                           _ptr_or_none(beta, "beta", _f32, (d,), dev), eps,
+                           _ptr(Y, "Y", t, shape, dev),
+                           _ptr_or_none(mean, "mean", _f32, (N,), dev),
+                           _ptr_or_none(rstd, "rstd", _f32, (N,), dev), _stream(stream))
+    _check(s, "fk_layer_norm")
 
 
 def layer_norm_backward_workspace(N: int, d: int, dtype=torch.float32, device="cuda"):
@@ -586,19 +610,19 @@ def fk_layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tenso
                            ws: torch.Tensor, stream=None):
     """Gradients of fk_layer_norm: dX (may be dY), dgamma and dbeta (fp32 [d]), each
     skipped when None."""
-    N, d = _matrix(X, "X")
-    _check(_lib.fk_layer_norm_backward(_dev(dY, "dY", X.dtype, (N, d)), _dev(X, "X"),
-                                       _dtype_code(X), N, d,
-                                       _opt(gamma, "gamma", torch.float32, (d,)),
-                                       _dev(mean, "mean", torch.float32, (N,)),
-                                       _dev(rstd, "rstd", torch.float32, (N,)),
-                                       _opt(dX, "dX", X.dtype, (N, d)),
-                                       _opt(dgamma, "dgamma", torch.float32, (d,)),
-                                       _opt(dbeta, "dbeta", torch.float32, (d,)),
-                                       _dev(ws, "ws", torch.uint8), ws.numel(),
-                                       (_here(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, ws),
-                                        _stream(stream))[1]),
-           "fk_layer_norm_backward")
+    dev = _home(X, "X")
+    N, d = shape = X.shape
+    t = X.dtype
+    s = _lib.fk_layer_norm_backward(_ptr(dY, "dY", t, shape, dev), _ptr(X, "X", t, shape, dev),
+                                    _point_code(t), N, d,
+                                    _ptr_or_none(gamma, "gamma", _f32, (d,), dev),
+                                    _ptr(mean, "mean", _f32, (N,), dev),
+                                    _ptr(rstd, "rstd", _f32, (N,), dev),
+                                    _ptr_or_none(dX, "dX", t, shape, dev),
+                                    _ptr_or_none(dgamma, "dgamma", _f32, (d,), dev),
+                                    _ptr_or_none(dbeta, "dbeta", _f32, (d,), dev),
+                                    _space(ws, dev), ws.numel(), _stream(stream))
+    _check(s, "fk_layer_norm_backward")
 
 
 def linear_workspace(N: int, d: int, m: int, dtype=torch.float32, device="cuda"):
@@ -612,6 +636,13 @@ def linear_backward_workspace(N: int, d: int, m: int, dtype=torch.float32, devic
                             (N, d, m, _point_code(dtype)), device)
 
 
+def _linear_sizes(X, W):
+    dev = _home(X, "X")
+    if not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("W must be a matrix")
+    return dev, X.shape, W.shape[0]
+
+
 def fk_linear(X: torch.Tensor, W: torch.Tensor, Y: torch.Tensor, ws: torch.Tensor,
               bias: torch.Tensor | None = None, act: str = "none",
               residual: torch.Tensor | None = None, Z: torch.Tensor | None = None,
@@ -619,15 +650,17 @@ def fk_linear(X: torch.Tensor, W: torch.Tensor, Y: torch.Tensor, ws: torch.Tenso
     """Y = act(X W^T + bias) + residual; X [N, d], W [m, d], Y [N, m] (may be residual); Z
     (optional) receives the pre-activation for fk_linear_backward.  act: "none", "relu",
     "gelu" or "silu"."""
-    N, d = _matrix(X, "X")
-    m = _matrix(W, "W")[0]
-    _check(_lib.fk_linear(_dev(X, "X"), _dtype_code(X), N, d, _dev(W, "W", X.dtype, (m, d)), m,
-                          _opt(bias, "bias", torch.float32, (m,)), _activation(act),
-                          _opt(residual, "residual", X.dtype, (N, m)),
-                          _dev(Y, "Y", X.dtype, (N, m)), _opt(Z, "Z", X.dtype, (N, m)),
-                          _dev(ws, "ws", torch.uint8), ws.numel(),
-                          (_here(X, W, bias, residual, Y, Z, ws), _stream(stream))[1]),
-           "fk_linear")
+    dev, shape, m = _linear_sizes(X, W)
+    N, d = shape
+    t = X.dtype
+    out = (N, m)
+    s = _lib.fk_linear(_ptr(X, "X", t, shape, dev), _point_code(t), N, d,
+                       _ptr(W, "W", t, (m, d), dev), m,
+                       _ptr_or_none(bias, "bias", _f32, (m,), dev), _activation(act),
+                       _ptr_or_none(residual, "residual", t, out, dev),
+                       _ptr(Y, "Y", t, out, dev), _ptr_or_none(Z, "Z", t, out, dev),
+                       _space(ws, dev), ws.numel(), _stream(stream))
+    _check(s, "fk_linear")
 
 
 def fk_linear_backward(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, ws: torch.Tensor,
@@ -636,33 +669,40 @@ def fk_linear_backward(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, ws: t
                        dbias: torch.Tensor | None = None, stream=None):
     """Gradients of fk_linear from dY [N, m] and, unless act is "none", the pre-activation
     Z it returned: dX [N, d], dW [m, d], dbias fp32 [m], each skipped when None."""
-    N, d = _matrix(X, "X")
-    m = _matrix(W, "W")[0]
-    _check(_lib.fk_linear_backward(_dev(dY, "dY", X.dtype, (N, m)), _dev(X, "X"),
-                                   _dtype_code(X), N, d, _dev(W, "W", X.dtype, (m, d)), m,
-                                   _activation(act), _opt(Z, "Z", X.dtype, (N, m)),
-                                   _opt(dX, "dX", X.dtype, (N, d)),
-                                   _opt(dW, "dW", X.dtype, (m, d)),
-                                   _opt(dbias, "dbias", torch.float32, (m,)),
-                                   _dev(ws, "ws", torch.uint8), ws.numel(),
-                                   (_here(dY, X, W, Z, dX, dW, dbias, ws),
-                                    _stream(stream))[1]),
-           "fk_linear_backward")
+    dev, shape, m = _linear_sizes(X, W)
+    N, d = shape
+    t = X.dtype
+    out = (N, m)
+    s = _lib.fk_linear_backward(_ptr(dY, "dY", t, out, dev), _ptr(X, "X", t, shape, dev),
+                                _point_code(t), N, d, _ptr(W, "W", t, (m, d), dev), m,
+                                _activation(act), _ptr_or_none(Z, "Z", t, out, dev),
+                                _ptr_or_none(dX, "dX", t, shape, dev),
+                                _ptr_or_none(dW, "dW", t, (m, d), dev),
+                                _ptr_or_none(dbias, "dbias", _f32, (m,), dev),
+                                _space(ws, dev), ws.numel(), _stream(stream))
+    _check(s, "fk_linear_backward")
+
+
+def _selection(labels, N=None):
+    if not isinstance(labels, torch.Tensor) or labels.dim() not in (1, 2):
+        raise ValueError("labels must be a tensor of [N] or [N, top]")
+    if N is None:
+        N = labels.shape[0]
+    return (N, 1 if labels.dim() == 1 else labels.shape[1],
+            (N,) if labels.dim() == 1 else (N, labels.shape[1]))
 
 
 def fk_balance_counts(labels: torch.Tensor, counts: torch.Tensor, rows: torch.Tensor,
                       stream=None):
     """counts (int32 [K]) of the cells selected by labels (int32 [N] or [N, top]; entries
     outside [0, K) select nothing) and rows (int32 [1]), the rows that select any."""
-    N = labels.shape[0]
-    top = labels.shape[1] if labels.dim() == 2 else 1
+    dev = _home(counts, "counts", 1)
+    N, top, shape = _selection(labels)
     K = counts.shape[0]
-    shape = (N, top) if labels.dim() == 2 else (N,)
-    _check(_lib.fk_balance_counts(_dev(labels, "labels", torch.int32, shape), N, top, K,
-                                  _dev(counts, "counts", torch.int32, (K,)),
-                                  _dev(rows, "rows", torch.int32, (1,)),
-                                  (_here(labels, counts, rows), _stream(stream))[1]),
-           "fk_balance_counts")
+    s = _lib.fk_balance_counts(_ptr(labels, "labels", _i32, shape, dev), N, top, K,
+                               _ptr(counts, "counts", _i32, (K,), dev),
+                               _ptr(rows, "rows", _i32, (1,), dev), _stream(stream))
+    _check(s, "fk_balance_counts")
 
 
 def balance_workspace(N: int, K: int, dtype=torch.float32, device="cuda"):
@@ -675,19 +715,18 @@ def fk_balance_loss(S: torch.Tensor, labels: torch.Tensor, counts: torch.Tensor,
                     ws: torch.Tensor, scale: float = 1.0, coef: float = 1.0, stream=None):
     """Balance loss (fp32 [1]) of the scores S [N, K] and its gradient dS (may be S; None
     skips it), with the counts and rows of fk_balance_counts."""
-    N, K = _matrix(S, "S")
-    top = labels.shape[1] if labels.dim() == 2 else 1
-    shape = (N, top) if labels.dim() == 2 else (N,)
-    _check(_lib.fk_balance_loss(_dev(S, "S"), _dtype_code(S), N, K,
-                                _dev(labels, "labels", torch.int32, shape), top,
-                                _dev(counts, "counts", torch.int32, (K,)),
-                                _dev(rows, "rows", torch.int32, (1,)), scale, coef,
-                                _dev(loss, "loss", torch.float32, (1,)),
-                                _opt(dS, "dS", S.dtype, (N, K)),
-                                _dev(ws, "ws", torch.uint8), ws.numel(),
-                                (_here(S, labels, counts, rows, loss, dS, ws),
-                                 _stream(stream))[1]),
-           "fk_balance_loss")
+    dev = _home(S, "S")
+    N, K = shape = S.shape
+    t = S.dtype
+    _, top, lshape = _selection(labels, N)
+    s = _lib.fk_balance_loss(_ptr(S, "S", t, shape, dev), _point_code(t), N, K,
+                             _ptr(labels, "labels", _i32, lshape, dev), top,
+                             _ptr(counts, "counts", _i32, (K,), dev),
+                             _ptr(rows, "rows", _i32, (1,), dev), scale, coef,
+                             _ptr(loss, "loss", _f32, (1,), dev),
+                             _ptr_or_none(dS, "dS", t, shape, dev), _space(ws, dev),
+                             ws.numel(), _stream(stream))
+    _check(s, "fk_balance_loss")
 
 
 class IvfFlatIndex:
