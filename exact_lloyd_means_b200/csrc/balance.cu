@@ -101,45 +101,58 @@ __device__ __forceinline__ bool row_selects(const LossArgs &a, int64_t i) {
     return false;
 }
 
-// The running softmax sums of some columns: maximum, sum of exp(x - m), and that sum
-// weighted by f.  m = -inf (with zero sums) where there is nothing but -inf; NaN anywhere
-// makes all NaN.
+// Softmax sums of some columns: the maximum score m, z = sum exp(scale (s - m)) and t = that
+// sum weighted by f (the exponentials as 2^(scale log2(e) (s - m)); the difference comes
+// first, so that scores at the type's lowest value do not overflow).  m = -inf (with zero
+// sums) where there is nothing but -inf; a NaN anywhere makes all NaN.
 struct Soft {
     float m, z, t;
-    __device__ __forceinline__ void join(float m2, float z2, float t2) {
-        const float mm = fmaxf(m, m2);
-        const float a = mm == -INFINITY ? 0.f : __expf(m - mm);
-        const float b = mm == -INFINITY ? 0.f : __expf(m2 - mm);
-        z = z * a + z2 * b;
-        t = t * a + t2 * b;
-        m = mm;
-    }
 };
 
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// What to subtract from scores below the maximum m (nothing but -inf: anything finite).
+__device__ __forceinline__ float soft_base(float m) { return m == -INFINITY ? 0.f : m; }
+
 template <int W>
-__device__ __forceinline__ void join_lanes(Soft &s) {
+__device__ __forceinline__ float lanes_max(float m) {
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1)
-        s.join(__shfl_xor_sync(0xffffffffu, s.m, o), __shfl_xor_sync(0xffffffffu, s.z, o),
-               __shfl_xor_sync(0xffffffffu, s.t, o));
+    for (int o = W / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+template <int W>
+__device__ __forceinline__ void lanes_sum(float &z, float &t) {
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) {
+        z += __shfl_xor_sync(0xffffffffu, z, o);
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+    }
 }
 
+// The group's sums from those of its threads: s.m is the maximum of this warp's part of the
+// group already, s.z and s.t this thread's sums against it.  For a group of several warps,
+// one barrier; lane l then holds warp l's sums.
 template <int TPR>
-__device__ __forceinline__ void join_group(Soft &s, Soft (*red)[kThreads / 32], int slot) {
-    join_lanes<(TPR < 32 ? TPR : 32)>(s);
+__device__ __forceinline__ Soft join_group(Soft s, float scale2, Soft (*red)[kThreads / 32], int slot) {
+    lanes_sum<(TPR < 32 ? TPR : 32)>(s.z, s.t);
     if constexpr (TPR > 32) {
-        constexpr int W = TPR / 32;
-        const int warp = threadIdx.x >> 5;
-        if ((threadIdx.x & 31) == 0) red[slot][warp] = s;
+        static_assert(TPR == kThreads, "one row a block");
+        constexpr int W = kThreads / 32;
+        if ((threadIdx.x & 31) == 0) red[slot][threadIdx.x >> 5] = s;
         __syncthreads();
-        const int w0 = warp / W * W;
-        s = red[slot][w0];
-#pragma unroll
-        for (int w = 1; w < W; ++w) {
-            const Soft o = red[slot][w0 + w];
-            s.join(o.m, o.z, o.t);
-        }
+        s = red[slot][threadIdx.x & (W - 1)];
+        const float m = lanes_max<W>(s.m);
+        const float c = exp2_fast(scale2 * (s.m - soft_base(m)));
+        s.z *= c;
+        s.t *= c;
+        lanes_sum<W>(s.z, s.t);
+        s.m = m;
     }
+    return s;
 }
 
 // part[block] = the block's sum of t_i (its rows in order, its groups in order); a single
@@ -162,19 +175,57 @@ __device__ __forceinline__ void finish_block(const LossArgs &a, const LossScales
     }
 }
 
+// f of the thread's columns j .. j + V - 1
+template <int V>
+__device__ __forceinline__ void load_shares(const LossArgs &a, const LossScales &c, int j,
+                                            float (&f)[V]) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = 0.f;
+    if (j >= a.K) return;
+    int32_t q[V];
+    bool done = false;
+    if constexpr (V % 4 == 0) {
+        if (a.cvec) {
+#pragma unroll
+            for (int k = 0; k < V; k += 4) {
+                const int4 u = *reinterpret_cast<const int4 *>(a.counts + j + k);
+                q[k] = u.x;
+                q[k + 1] = u.y;
+                q[k + 2] = u.z;
+                q[k + 3] = u.w;
+            }
+            done = true;
+        }
+    }
+    if (!done) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) q[k] = a.counts[j + k];
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = static_cast<float>(q[k]) * c.unit;
+}
+
+// Up to 16 columns a thread, f stays in registers for all rows of the block.
 template <typename T, int V, int NV, int TPR>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, NV * V <= 8 ? 4 : (NV * V <= 16 ? 3 : 2))
     balance_loss_kernel(const T *S, T *dS, const LossArgs a) {
     __shared__ Soft red[2][kThreads / 32];
     __shared__ double sums[kThreads];
     pdl_wait();
     pdl_trigger();
     constexpr int G = kThreads / TPR;
+    constexpr bool KEEP_F = NV * V <= 16;
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const LossScales c(a);
+    const float scale2 = a.scale * 1.44269504f;
     double total = 0.0;
     int slot = 0;
     Raw<T, V> x[NV];
+    float f[KEEP_F ? NV : 1][V];
+    if constexpr (KEEP_F) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) load_shares<V>(a, c, (n * TPR + t) * V, f[n]);
+    }
     bool keep = false;
     // padding rows are read like the others (their values are not used)
     auto fetch = [&](int64_t i) {
@@ -192,75 +243,50 @@ __global__ void __launch_bounds__(kThreads)
         const int64_t i = i0 + grp;
         const bool on = keep;
         float e[NV][V];
-        Soft s{-INFINITY, 0.f, 0.f};
-        float mine = -INFINITY;
-        bool nan = false;
+        float m = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const bool in = on && (n * TPR + t) * V < a.K;
             x[n].get(e[n]);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                e[n][k] = in ? a.scale * e[n][k] : -INFINITY;
-                nan |= e[n][k] != e[n][k];
-                mine = fmaxf(mine, e[n][k]);
+                e[n][k] = in ? e[n][k] : -INFINITY;
+                m = max_nan(m, e[n][k]);
             }
         }
-        if (nan) mine = NAN;
         if (i0 + step < a.N) fetch(i0 + step + grp);
-        float f[NV][V];
+        m = lanes_max<(TPR < 32 ? TPR : 32)>(m);
+        Soft s{m, 0.f, 0.f};
+        const float base = soft_base(m);
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int j = (n * TPR + t) * V;
+            float g[V];
+            if constexpr (!KEEP_F) load_shares<V>(a, c, (n * TPR + t) * V, g);
 #pragma unroll
-            for (int k = 0; k < V; ++k) f[n][k] = 0.f;
-            if (j < a.K) {
-                int32_t q[V];
-                if (V % 4 == 0 && a.cvec) {
-#pragma unroll
-                    for (int k = 0; k < V; k += 4) {
-                        const int4 u = *reinterpret_cast<const int4 *>(a.counts + j + k);
-                        q[k] = u.x;
-                        if constexpr (V > 1) {
-                            q[k + 1] = u.y;
-                            q[k + 2] = u.z;
-                            q[k + 3] = u.w;
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < V; ++k) q[k] = a.counts[j + k];
-                }
-#pragma unroll
-                for (int k = 0; k < V; ++k) f[n][k] = static_cast<float>(q[k]) * c.unit;
-            }
-            if (mine != -INFINITY) {
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    e[n][k] = __expf(e[n][k] - mine);
-                    s.z += e[n][k];
-                    s.t += e[n][k] * f[n][k];
-                }
+            for (int k = 0; k < V; ++k) {
+                e[n][k] = exp2_fast(scale2 * (e[n][k] - base));
+                s.z += e[n][k];
+                s.t += e[n][k] * (KEEP_F ? f[KEEP_F ? n : 0][k] : g[k]);
             }
         }
-        s.m = mine;
-        join_group<TPR>(s, red, slot);
+        s = join_group<TPR>(s, scale2, red, slot);
         slot ^= 1;
-        const bool none = s.m == -INFINITY;
-        const float inv = none ? 0.f : 1.f / s.z;
+        const float inv = s.m == -INFINITY ? 0.f : 1.f / s.z;
         const float ti = s.t * inv;
         if (t == 0 && on) total += ti;
         if (dS != nullptr && i < a.N) {
-            const float own = none || mine == -INFINITY ? 0.f : __expf(mine - s.m) * inv;
-            const float gp = c.gc * own;
+            // this warp's exponentials against the group's maximum, over the sum
+            const float gp = TPR > 32 ? c.gc * exp2_fast(scale2 * (m - soft_base(s.m))) * inv : c.gc * inv;
+            const float gt = -ti * gp;
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
                 const int j = (n * TPR + t) * V;
                 if (j < a.K) {
-                    float v[V];
+                    float v[V], g[V];
+                    if constexpr (!KEEP_F) load_shares<V>(a, c, j, g);
 #pragma unroll
                     for (int k = 0; k < V; ++k)
-                        v[k] = own == 0.f ? 0.f : gp * e[n][k] * (f[n][k] - ti);
+                        v[k] = e[n][k] * ((KEEP_F ? f[KEEP_F ? n : 0][k] : g[k]) * gp + gt);
                     Raw<T, V>::put(dS + i * a.K + j, v);
                 }
             }
@@ -269,7 +295,8 @@ __global__ void __launch_bounds__(kThreads)
     finish_block(a, c, total, t == 0, sums);
 }
 
-// Rows longer than a block's registers: one block a row, read twice.
+// Rows longer than a block's registers: one block a row, read once for the maximum, once for
+// the sums and once for the gradient.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     balance_long_kernel(const T *S, T *dS, const LossArgs a) {
@@ -278,6 +305,7 @@ __global__ void __launch_bounds__(kThreads)
     pdl_wait();
     pdl_trigger();
     const LossScales c(a);
+    const float scale2 = a.scale * 1.44269504f;
     double total = 0.0;
     int slot = 0;
     for (int64_t i = blockIdx.x; i < a.N; i += gridDim.x) {
@@ -289,19 +317,22 @@ __global__ void __launch_bounds__(kThreads)
             continue;
         }
         Soft r{-INFINITY, 0.f, 0.f};
+        for (int64_t j = threadIdx.x; j < a.K; j += kThreads)
+            r.m = max_nan(r.m, head_load(s + j));
+        r.m = lanes_max<32>(r.m);
         for (int64_t j = threadIdx.x; j < a.K; j += kThreads) {
-            const float v = a.scale * head_load(s + j);
-            if (v != -INFINITY) r.join(v, 1.f, static_cast<float>(a.counts[j]) * c.unit);
+            const float e = exp2_fast(scale2 * (head_load(s + j) - soft_base(r.m)));
+            r.z += e;
+            r.t += e * (static_cast<float>(a.counts[j]) * c.unit);
         }
-        join_group<kThreads>(r, red, slot);
+        r = join_group<kThreads>(r, scale2, red, slot);
         slot ^= 1;
-        const bool none = r.m == -INFINITY;
-        const float inv = none ? 0.f : 1.f / r.z;
+        const float inv = r.m == -INFINITY ? 0.f : 1.f / r.z;
         const float ti = r.t * inv;
         if (threadIdx.x == 0) total += ti;
         if (dS)
             for (int64_t j = threadIdx.x; j < a.K; j += kThreads) {
-                const float p = none ? 0.f : __expf(a.scale * head_load(s + j) - r.m) * inv;
+                const float p = exp2_fast(scale2 * (head_load(s + j) - soft_base(r.m))) * inv;
                 head_store(dS + i * a.K + j,
                            c.gc * p * (static_cast<float>(a.counts[j]) * c.unit - ti));
             }

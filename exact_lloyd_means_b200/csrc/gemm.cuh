@@ -31,29 +31,29 @@ struct GemmArgs {
     int act;
     const void *R;
     void *C, *Z;
-    float *part;  // [splits][rows][round_up(cols, 4)] when splits > 1
+    float *part;  // [splits][rows][round_up(cols, 8)] when splits > 1
     uint32_t *err;
 };
 
 GemmPlan gemm_plan(int64_t rows, int64_t cols, int64_t depth, int planes);
 inline size_t gemm_part_bytes(int64_t rows, int64_t cols, const GemmPlan &p) {
-    return p.splits > 1 ? sizeof(float) * p.splits * rows * round_up(cols, 4) : 0;
+    return p.splits > 1 ? sizeof(float) * p.splits * rows * round_up(cols, 8) : 0;
 }
 cudaError_t launch_gemm(const GemmArgs &a, const GemmPlan &p, cudaStream_t st);
 
 // ----------------------------------------------------------------- epilogue
-template <int V>
-__device__ __forceinline__ void act_values(float (&z)[V], int act) {
+template <int P, int V>
+__device__ __forceinline__ void act_values(float (&z)[P][V], int act) {
     if (act == FK_ACT_NONE) return;
     if (act == FK_ACT_RELU) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) z[j] = act_value(z[j], FK_ACT_RELU);
+        for (int i = 0; i < P * V; ++i) z[i / V][i % V] = act_value(z[i / V][i % V], FK_ACT_RELU);
     } else if (act == FK_ACT_GELU) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) z[j] = act_value(z[j], FK_ACT_GELU);
+        for (int i = 0; i < P * V; ++i) z[i / V][i % V] = act_value(z[i / V][i % V], FK_ACT_GELU);
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) z[j] = act_value(z[j], FK_ACT_SILU);
+        for (int i = 0; i < P * V; ++i) z[i / V][i % V] = act_value(z[i / V][i % V], FK_ACT_SILU);
     }
 }
 
@@ -63,64 +63,61 @@ struct Epilogue {
     void *C, *Z;
     int64_t cols;
     int act;
-    int vec;  // rows of C, Z and R start on 16-byte boundaries
 };
 
-// The residual of V columns, read before anything of the row is written (C may be R).
-template <typename T>
-__device__ __forceinline__ uint4 epilogue_residual(const Epilogue &e, int64_t row, int64_t col) {
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (e.R == nullptr) return u;
-    const T *r = static_cast<const T *>(e.R) + row * e.cols + col;
-    if (e.vec) return *reinterpret_cast<const uint4 *>(r);
-    T *t = reinterpret_cast<T *>(&u);
-#pragma unroll
-    for (int j = 0; j < kVec<T>; ++j)
-        if (col + j < e.cols) t[j] = r[j];
-    return u;
-}
+// P pieces of V consecutive columns of the output: piece p starts at element at + p * step of the
+// output, in column col + p * cstep; it exists if bit p of `in` is set (or ALL of them do).
+struct Pieces {
+    int64_t at, step, col;
+    int cstep;
+    uint32_t in;
+};
 
-template <typename T>
-__device__ __forceinline__ void epilogue_bias(const Epilogue &e, int64_t col,
-                                              float (&b)[kVec<T>]) {
+// z: their products without the bias.  Each output is rounded once from fp32.  The residual
+// is read before anything of the pieces is written (C may be R).  The additions
+// are kept apart from the activation's products, so that the bits do not depend on which
+// outputs are asked for; the activation is one branch for all pieces, which keeps their
+// chains of dependent instructions side by side.
+template <typename T, int V, bool ALL, int P>
+__device__ __forceinline__ void epilogue_pieces(const Epilogue &e, const Pieces &o, int bvec,
+                                                float (&z)[P][V]) {
+    Raw<T, V> res[P];
+    if (e.R != nullptr) {
 #pragma unroll
-    for (int j = 0; j < kVec<T>; ++j)
-        b[j] = e.bias != nullptr && col + j < e.cols ? e.bias[col + j] : 0.f;
-}
-
-template <typename T>
-__device__ __forceinline__ void epilogue_put(T *row, int64_t col, int64_t cols, int vec,
-                                             const uint4 &u) {
-    if (vec) {
-        *reinterpret_cast<uint4 *>(row + col) = u;
-        return;
+        for (int p = 0; p < P; ++p) {
+            res[p].zero();
+            if (ALL || (o.in >> p & 1u)) res[p].load(static_cast<const T *>(e.R) + o.at + p * o.step);
+        }
     }
-    const T *t = reinterpret_cast<const T *>(&u);
+    if (e.bias != nullptr) {
 #pragma unroll
-    for (int j = 0; j < kVec<T>; ++j)
-        if (col + j < cols) row[col + j] = t[j];
-}
-
-// z: products without the bias.  Each output is rounded once from fp32 (the additions are kept
-// apart from the activation's products, so that the bits do not depend on which outputs are
-// asked for).
-template <typename T>
-__device__ __forceinline__ void epilogue_store(const Epilogue &e, int64_t row, int64_t col,
-                                               float (&z)[kVec<T>],
-                                               const float (&b)[kVec<T>], const uint4 &r) {
-    constexpr int V = kVec<T>;
+        for (int p = 0; p < P; ++p) {
+            if (ALL || (o.in >> p & 1u)) {
+                float b[V];
+                load_params<V>(e.bias + o.col + p * o.cstep, bvec, b);
 #pragma unroll
-    for (int j = 0; j < V; ++j) z[j] = __fadd_rn(z[j], b[j]);
-    if (e.Z != nullptr)
-        epilogue_put(static_cast<T *>(e.Z) + row * e.cols, col, e.cols, e.vec, pack16(z));
+                for (int j = 0; j < V; ++j) z[p][j] = __fadd_rn(z[p][j], b[j]);
+            }
+        }
+    }
+    if (e.Z != nullptr) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            if (ALL || (o.in >> p & 1u)) Raw<T, V>::put(static_cast<T *>(e.Z) + o.at + p * o.step, z[p]);
+    }
     act_values(z, e.act);
     if (e.R != nullptr) {
-        float rv[V];
-        unpack16(r, rv);
 #pragma unroll
-        for (int j = 0; j < V; ++j) z[j] = __fadd_rn(z[j], rv[j]);
+        for (int p = 0; p < P; ++p) {
+            float r[V];
+            res[p].get(r);
+#pragma unroll
+            for (int j = 0; j < V; ++j) z[p][j] = __fadd_rn(z[p][j], r[j]);
+        }
     }
-    epilogue_put(static_cast<T *>(e.C) + row * e.cols, col, e.cols, e.vec, pack16(z));
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+        if (ALL || (o.in >> p & 1u)) Raw<T, V>::put(static_cast<T *>(e.C) + o.at + p * o.step, z[p]);
 }
 
 }  // namespace fk

@@ -7,9 +7,10 @@
 //   * warp 0: TMA producer, a ring of stages of 64 of the depth; warp 1: tcgen05.mma issuer,
 //     two accumulators in tensor memory, so that a tile's epilogue overlaps the next tile's
 //     products; warps 2..9: epilogue, two groups of four warps, half the columns each.  A
-//     warp takes 32 rows x 32 columns from tensor memory through its own 4 KB of shared
-//     memory (16-byte chunks XORed with the row, no bank conflicts), so that every global
-//     access (residual, pre-activation, output) is 16 bytes a lane along a row;
+//     thread has one row of the tile and takes 32 columns at a time; it reads and writes
+//     them in whole 32-byte sectors.  Nothing passes through shared memory, whose bandwidth
+//     the operands take (128 x 64 by 256 x 64 a chunk written and read): staging the tile
+//     there as fp32 took 92 us where this takes 73 (10,000 x 768 x 4096, GELU, both outputs);
 //   * either operand may be stored along the depth (K-major) or along its rows (MN-major):
 //     both are 128-byte-swizzled TMA boxes, and the MMA descriptors say which.  So the three
 //     products of a linear layer and its gradients read their operands as they lie;
@@ -31,21 +32,24 @@ namespace {
 
 constexpr int kBandRows = 8;  // tiles of one column band that run side by side
 
-template <int CG, int BN>
+// OV = consecutive columns an epilogue thread writes at once: 32 or 16 bytes of them, or one
+// column, where rows of the outputs do not start on such boundaries.
+template <int CG, int BN, int OV>
 struct GemmCfg {
     static constexpr int kABytes = kBM * kBK * 2;
     static constexpr int kBRows = BN / CG;
     static constexpr int kBBytes = kBRows * kBK * 2;
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = CG == 2 ? 6 : (BN == 128 ? 6 : 8);
     static constexpr int kEpiWarps = 8;
-    static constexpr int kStageOut = 32 * 32 * 4;  // one warp's 32 x 32 fp32
+    static constexpr int kStageOut = OV == 1 ? 32 * 33 * 4 : 0;  // a warp's 32 x 32 fp32
     static constexpr int kBarBytes = 256;
+    static constexpr int kSpace = 232448 - 1024 - kBarBytes - kEpiWarps * kStageOut;
+    static constexpr int kStages = kSpace / kStageBytes < 8 ? kSpace / kStageBytes : 8;
     static constexpr int kSmemBytes =
         kStages * kStageBytes + kEpiWarps * kStageOut + kBarBytes + 1024;
     static constexpr int kThreads = 64 + kEpiWarps * 32;
     static constexpr int kTmemCols = 2 * BN;
-    static constexpr int kGroupCols = BN / 2;  // columns of one epilogue group
+    static constexpr int kGroupCols = BN / (kEpiWarps / 4);  // columns of one epilogue group
     static_assert(kSmemBytes <= 232448, "shared memory");
     static_assert(kStageBytes % 1024 == 0, "stage bases stay 1024-byte aligned");
     static_assert(8 * (2 * kStages + 5) + 8 <= kBarBytes, "barriers");
@@ -97,12 +101,12 @@ __device__ __forceinline__ void gemm_timeout(volatile uint32_t *abort_flag, uint
     err[0] = kErrTimeout;
 }
 
-template <int CG, int BN, typename T>
-__global__ void __launch_bounds__(GemmCfg<CG, BN>::kThreads, 1)
+template <int CG, int BN, typename T, int OV>
+__global__ void __launch_bounds__(GemmCfg<CG, BN, OV>::kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                const GemmShape sh, const Epilogue ep, float *__restrict__ part,
+                const GemmShape sh, const Epilogue ep, int bvec, float *__restrict__ part,
                 uint32_t *__restrict__ err, uint64_t wait_ns) {
-    using Cfg = GemmCfg<CG, BN>;
+    using Cfg = GemmCfg<CG, BN, OV>;
     constexpr int S = Cfg::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -272,15 +276,13 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN>::kThreads, 1)
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        constexpr int V = kVec<T>;
-        constexpr int LPR = 32 / V;            // lanes per row of 32 columns
-        constexpr int RPP = 32 / LPR;          // rows per pass
+        // thread = row of the tile (tensor-memory lane); 32 columns at a time
         const int g = (warp - 2) >> 2;
         const int q = warp & 3;
-        float4 *st = reinterpret_cast<float4 *>(stage_out + (warp - 2) * Cfg::kStageOut);
+        [[maybe_unused]] float *st =
+            reinterpret_cast<float *>(stage_out + (warp - 2) * Cfg::kStageOut);
         const uint32_t tempty_c =
             CG == 2 ? ptx::mapa_shared(ptx::smem_u32(tempty), 0) : 0u;
-        const int lr = lane / LPR, lc = (lane % LPR) * V;
         uint32_t it = 0;
         for (int64_t u = first; u < sh.units; u += step, ++it) {
             const Unit un = unit_of<CG>(sh, u);
@@ -298,18 +300,7 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN>::kThreads, 1)
                                 g * Cfg::kGroupCols;
 #pragma unroll 1
             for (int c = 0; c < Cfg::kGroupCols / 32; ++c) {
-                const int64_t col = c0 + c * 32 + lc;
-                const bool in = col < sh.cols;
-                uint4 res[RPP == 8 ? 4 : 8];
-                constexpr int P = 32 / RPP;
-                if (sh.splits == 1) {
-#pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        const int64_t row = r0 + p * RPP + lr;
-                        res[p] = in && row < sh.rows ? epilogue_residual<T>(ep, row, col)
-                                                     : make_uint4(0u, 0u, 0u, 0u);
-                    }
-                }
+                const int64_t col = c0 + c * 32;
                 __syncwarp();
                 float v[32];
                 ptx::tmem_ld32_sync(tb + c * 32, v);
@@ -323,41 +314,48 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN>::kThreads, 1)
                             ptx::mbar_arrive(&tempty[acc]);
                     }
                 }
+                if (sh.splits > 1) {  // fp32 partial products, rows of a multiple of 8
+                    if (r0 + lane < sh.rows) {
+                        float *dst = part + (un.split * sh.rows + r0 + lane) * sh.part_ld + col;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    st[lane * 8 + (j ^ (lane & 7))] =
-                        make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                __syncwarp();
-                if (sh.splits == 1) {
-                    float b[V];
-                    epilogue_bias<T>(ep, col, b);
-#pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        const int lrow = p * RPP + lr;
-                        const int64_t row = r0 + lrow;
-                        float z[V];
-#pragma unroll
-                        for (int j = 0; j < V / 4; ++j) {
-                            const float4 f = st[lrow * 8 + ((lc / 4 + j) ^ (lrow & 7))];
-                            z[4 * j] = f.x;
-                            z[4 * j + 1] = f.y;
-                            z[4 * j + 2] = f.z;
-                            z[4 * j + 3] = f.w;
+                        for (int j = 0; j < 32; j += 8) {
+                            if (col + j < sh.part_ld) {
+                                const float o[8] = {v[j],     v[j + 1], v[j + 2], v[j + 3],
+                                                    v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
+                                Raw<float, 8>::put(dst + j, o);
+                            }
                         }
-                        if (in && row < sh.rows) epilogue_store<T>(ep, row, col, z, b, res[p]);
                     }
-                } else {  // fp32 partial products, four columns a lane
-                    float *dst = part + un.split * sh.rows * sh.part_ld;
+                } else if constexpr (OV > 1) {
+                    float z[32 / OV][OV];
 #pragma unroll
-                    for (int p = 0; p < 8; ++p) {
-                        const int lrow = p * 4 + lane / 8;
-                        const int64_t row = r0 + lrow, pc = c0 + c * 32 + (lane & 7) * 4;
-                        if (row < sh.rows && pc < sh.part_ld)
-                            *reinterpret_cast<float4 *>(dst + row * sh.part_ld + pc) =
-                                st[lrow * 8 + ((lane & 7) ^ (lrow & 7))];
+                    for (int j = 0; j < 32; ++j) z[j / OV][j % OV] = v[j];
+                    Pieces o{(r0 + lane) * sh.cols + col, OV, col, OV, 0u};
+                    const int64_t left = (sh.cols - col) / OV;  // pieces before the last column
+                    if (r0 + lane >= sh.rows || left <= 0) continue;
+                    if (left >= 32 / OV) {
+                        epilogue_pieces<T, OV, true>(ep, o, bvec, z);
+                    } else {
+                        o.in = (1u << left) - 1u;
+                        epilogue_pieces<T, OV, false>(ep, o, bvec, z);
                     }
+                } else {  // turned in shared memory: thread = column, so that rows are coalesced
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) st[lane * 33 + j] = v[j];
+                    __syncwarp();
+#pragma unroll 1
+                    for (int rr = 0; rr < 32; rr += 8) {
+                        float z[8][1];
+#pragma unroll
+                        for (int p = 0; p < 8; ++p) z[p][0] = st[(rr + p) * 33 + lane];
+                        const int64_t left = sh.rows - (r0 + rr);
+                        const uint32_t n = left <= 0 ? 0u : (left < 8 ? (1u << left) - 1u : 0xffu);
+                        const Pieces o{(r0 + rr) * sh.cols + col + lane, sh.cols, col + lane, 0,
+                                       col + lane < sh.cols ? n : 0u};
+                        epilogue_pieces<T, 1, false>(ep, o, 0, z);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         }
     }
@@ -384,37 +382,29 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN>::kThreads, 1)
 }
 
 // Join the partial products of a split depth, in order, and apply the epilogue.
-template <typename T>
+template <typename T, int V>
 __global__ void __launch_bounds__(256)
     gemm_join_kernel(const float *__restrict__ part, int splits, int64_t rows, int64_t part_ld,
-                     int64_t per_row, const Epilogue ep) {
-    constexpr int V = kVec<T>;
+                     int64_t per_row, const Epilogue ep, int bvec) {
     pdl_wait();
     pdl_trigger();
     const int64_t total = rows * per_row;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < total;
          t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
         const int64_t row = t / per_row, col = (t - row * per_row) * V;
-        const uint4 r = epilogue_residual<T>(ep, row, col);
-        float b[V], z[V];
-        epilogue_bias<T>(ep, col, b);
+        const Pieces o{row * ep.cols + col, 0, col, 0, 1u};
+        float z[1][V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) z[j] = 0.f;
+        for (int j = 0; j < V; ++j) z[0][j] = 0.f;
         const float *p = part + row * part_ld + col;
+#pragma unroll 4
         for (int s = 0; s < splits; ++s) {
+            float f[V];
+            load_params<V>(p + s * rows * part_ld, 1, f);
 #pragma unroll
-            for (int j = 0; j < V; j += 4) {
-                if (col + j < part_ld) {
-                    const float4 f = *reinterpret_cast<const float4 *>(p + j);
-                    z[j] += f.x;
-                    z[j + 1] += f.y;
-                    z[j + 2] += f.z;
-                    z[j + 3] += f.w;
-                }
-            }
-            p += rows * part_ld;
+            for (int j = 0; j < V; ++j) z[0][j] += f[j];
         }
-        epilogue_store<T>(ep, row, col, z, b, r);
+        epilogue_pieces<T, V, true>(ep, o, bvec, z);
     }
 }
 
@@ -435,10 +425,10 @@ bool operand_map(CUtensorMap *m, const GemmOperand &o, int64_t outer, int64_t in
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CG, int BN, typename T>
+template <int CG, int BN, typename T, int OV>
 cudaError_t launch_cfg(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
-    using Cfg = GemmCfg<CG, BN>;
-    auto kernel = gemm_kernel<CG, BN, T>;
+    using Cfg = GemmCfg<CG, BN, OV>;
+    auto kernel = gemm_kernel<CG, BN, T, OV>;
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t e = smem_opt_in(kernel, Cfg::kSmemBytes, smem_set);
     if (e != cudaSuccess) return e;
@@ -460,7 +450,8 @@ cudaError_t launch_cfg(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
     s.tiles_r = ceil_div(a.rows, kBM * CG);
     s.tiles_c = ceil_div(a.cols, BN);
     s.units = s.tiles_r * s.tiles_c * p.splits;
-    s.part_ld = round_up(a.cols, 4);
+    s.part_ld = round_up(a.cols, 8);
+    const int bvec = aligned(a.bias, 16);
     Epilogue ep{};
     ep.bias = a.bias;
     ep.R = a.R;
@@ -468,8 +459,6 @@ cudaError_t launch_cfg(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
     ep.Z = a.Z;
     ep.cols = a.cols;
     ep.act = a.act;
-    ep.vec = (a.cols * static_cast<int64_t>(sizeof(T))) % 16 == 0 && aligned(a.C, 16) &&
-             aligned(a.Z, 16) && aligned(a.R, 16);
     const int64_t slots = device_sm_count() / CG;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(CG * (s.units < slots ? s.units : slots)));
@@ -485,25 +474,39 @@ cudaError_t launch_cfg(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 2 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, tA, tB, s, ep, a.part, a.err, kDefaultWaitNs);
+    e = cudaLaunchKernelEx(&cfg, kernel, tA, tB, s, ep, bvec, a.part, a.err, kDefaultWaitNs);
     if (e != cudaSuccess) return e;
     note_launch();
     if (p.splits > 1) {
-        const int64_t work = a.rows * ceil_div(a.cols, kVec<T>);
-        const int64_t g = ceil_div(work, 256), cap = static_cast<int64_t>(device_sm_count()) * 8;
-        e = launch_pdl(gemm_join_kernel<T>, dim3(static_cast<unsigned>(g < cap ? g : cap)),
+        constexpr int JV = OV > kVec<T> ? kVec<T> : OV;  // 16 bytes of output a thread
+        const int64_t per_row = ceil_div(a.cols, JV);
+        const int64_t g = ceil_div(a.rows * per_row, 256),
+                      cap = static_cast<int64_t>(device_sm_count()) * 8;
+        e = launch_pdl(gemm_join_kernel<T, JV>, dim3(static_cast<unsigned>(g < cap ? g : cap)),
                        dim3(256), 0, st, static_cast<const float *>(a.part), p.splits, a.rows,
-                       s.part_ld, ceil_div(a.cols, kVec<T>), ep);
+                       s.part_ld, per_row, ep, bvec);
         if (e == cudaSuccess) note_launch();
     }
     return e;
 }
 
+template <typename T, int OV>
+cudaError_t launch_v(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
+    if (p.cg == 2) return launch_cfg<2, 256, T, OV>(a, p, st);
+    if (p.bn == 128) return launch_cfg<1, 128, T, OV>(a, p, st);
+    return launch_cfg<1, 64, T, OV>(a, p, st);
+}
+
 template <typename T>
 cudaError_t launch_t(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
-    if (p.cg == 2) return launch_cfg<2, 256, T>(a, p, st);
-    if (p.bn == 128) return launch_cfg<1, 128, T>(a, p, st);
-    return launch_cfg<1, 64, T>(a, p, st);
+    constexpr int V = kVec<T>;
+    auto rows_on = [&](int v) {
+        const size_t b = v * sizeof(T);
+        return a.cols % v == 0 && aligned(a.C, b) && aligned(a.Z, b) && aligned(a.R, b);
+    };
+    if (rows_on(2 * V)) return launch_v<T, 2 * V>(a, p, st);
+    if (rows_on(V)) return launch_v<T, V>(a, p, st);
+    return launch_v<T, 1>(a, p, st);
 }
 
 }  // namespace
@@ -531,7 +534,7 @@ GemmPlan gemm_plan(int64_t rows, int64_t cols, int64_t depth, int planes) {
             double cost = waves * (static_cast<double>(ceil_div(nkc, s)) * terms * c.cycles) +
                           4000 + 500 * waves;
             if (s > 1)
-                cost += 4000 + 8.0 * s * static_cast<double>(rows) * round_up(cols, 4) / 3000;
+                cost += 4000 + 8.0 * s * static_cast<double>(rows) * round_up(cols, 8) / 3000;
             if (best_cost < 0 || cost < best_cost) {
                 best_cost = cost;
                 best = GemmPlan{c.cg, c.bn, s};

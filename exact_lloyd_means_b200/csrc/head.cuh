@@ -69,6 +69,42 @@ struct Raw<T, kVec<T>> {
         *reinterpret_cast<uint4 *>(p) = pack16(v);
     }
 };
+// 32 bytes: one whole sector of memory for each thread of a warp that walks down rows.
+template <typename T>
+struct Raw<T, 2 * kVec<T>> {
+    uint4 u[2];
+    __device__ __forceinline__ void load(const T *p) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(u[0].x), "=r"(u[0].y), "=r"(u[0].z), "=r"(u[0].w), "=r"(u[1].x),
+                       "=r"(u[1].y), "=r"(u[1].z), "=r"(u[1].w)
+                     : "l"(p)
+                     : "memory");
+    }
+    __device__ __forceinline__ void zero() { u[0] = u[1] = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void get(float (&v)[2 * kVec<T>]) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float t[kVec<T>];
+            unpack16(u[h], t);
+#pragma unroll
+            for (int j = 0; j < kVec<T>; ++j) v[h * kVec<T> + j] = t[j];
+        }
+    }
+    static __device__ __forceinline__ void put(T *p, const float (&v)[2 * kVec<T>]) {
+        uint4 w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float t[kVec<T>];
+#pragma unroll
+            for (int j = 0; j < kVec<T>; ++j) t[j] = v[h * kVec<T> + j];
+            w[h] = pack16(t);
+        }
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+                     "r"(w[0].x), "r"(w[0].y), "r"(w[0].z), "r"(w[0].w), "r"(w[1].x),
+                     "r"(w[1].y), "r"(w[1].z), "r"(w[1].w)
+                     : "memory");
+    }
+};
 template <typename T>
 struct Raw<T, 1> {
     T u;
@@ -159,21 +195,58 @@ size_t linear_backward_ws_bytes(int64_t N, int d, int m, fk_dtype dtype);
 cudaError_t launch_linear(const LinearArgs &a, void *ws, cudaStream_t st);
 cudaError_t launch_linear_backward(const LinearArgs &a, void *ws, cudaStream_t st);
 
+// 1 / x and 2^x by the special function unit, subnormal results flushed: a few units of 2^-24,
+// one instruction each (the forms that keep subnormals take several more).
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Half the complementary error function at |z| / sqrt(2), so that the normal distribution
+// function Phi(z) is 1 - h for z > 0 and h otherwise, and e = exp(-z^2 / 2).  Abramowitz and
+// Stegun 7.1.26: erf within 1.5e-7, so Phi within 0.75e-7 (1.3 units of 2^-24), in two special
+// function calls and about ten products; with CUDA's erff, several times the instructions,
+// the epilogue of a 768-deep product is bound by its arithmetic.
+__device__ __forceinline__ float half_erfc(float z, float *e) {
+    const float t = rcp_fast(1.f + 0.23164190f * fabsf(z));  // 0.3275911 / sqrt(2)
+    float p = 0.5f * 1.061405429f;
+    p = p * t - 0.5f * 1.453152027f;
+    p = p * t + 0.5f * 1.421413741f;
+    p = p * t - 0.5f * 0.284496736f;
+    p = p * t + 0.5f * 0.254829592f;
+    *e = exp2_fast(-0.72134752f * z * z);
+    return p * t * *e;
+}
+
 // act(z): relu max(z, 0); GELU z Phi(z) with the normal distribution function Phi (the
-// erf form); SiLU z / (1 + exp(-z)).
+// erf form); SiLU z / (1 + exp(-z)).  NaN stays NaN; at infinity, the
+// limits of GELU, and for SiLU what its formula gives.
 __device__ __forceinline__ float act_value(float z, int act) {
     if (act == FK_ACT_RELU) return z > 0.f ? z : (z == z ? 0.f : z);
-    if (act == FK_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
-    if (act == FK_ACT_SILU) return z / (1.f + expf(-z));
+    if (act == FK_ACT_GELU) {
+        float e;
+        const float h = half_erfc(z, &e);
+        return fmaxf(z, 0.f) - fminf(fabsf(z), 32.f) * h;  // (h = 0 long before 32; NaN stays)
+    }
+    if (act == FK_ACT_SILU) return z * rcp_fast(1.f + exp2_fast(-1.44269504f * z));
     return z;
 }
 // act'(z); the slope of relu at 0 is 0.
 __device__ __forceinline__ float act_slope(float z, int act) {
     if (act == FK_ACT_RELU) return z > 0.f ? 1.f : (z == z ? 0.f : z);
-    if (act == FK_ACT_GELU)
-        return 0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * expf(-0.5f * z * z);
+    if (act == FK_ACT_GELU) {
+        float e;
+        const float h = half_erfc(z, &e);
+        return (z > 0.f ? 1.f - h : h) + z * 0.39894228f * e;
+    }
     if (act == FK_ACT_SILU) {
-        const float s = 1.f / (1.f + expf(-z));
+        const float s = rcp_fast(1.f + exp2_fast(-1.44269504f * z));
         return s * (1.f + z * (1.f - s));
     }
     return 1.f;
