@@ -12,11 +12,14 @@
 // weighted sum sum f exp(x - m) of its own columns, and the group joins them (rescaled to
 // the common maximum).  A row whose scores are all -inf has p = 0.
 #include "head.cuh"
+#include "ptx_sm100.cuh"
 
 namespace fk {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxStages = 8;         // slots of the ring of rows
+constexpr int kRingBytes = 64 << 10;  // its size: two or three blocks an SM
 constexpr int kOneBlockLabels = 1 << 15;  // counted by one block in one launch
 constexpr int kSharedCells = 12288;       // counters kept in shared memory (48 KB)
 
@@ -77,7 +80,6 @@ struct LossArgs {
     int K, top;
     const int32_t *labels, *counts, *rows;
     float scale, coef;
-    int cvec;  // counts start on a 16-byte boundary
     float *loss;
     double *part;
 };
@@ -120,31 +122,41 @@ __device__ __forceinline__ float soft_base(float m) { return m == -INFINITY ? 0.
 
 template <int W>
 __device__ __forceinline__ float lanes_max(float m) {
+    if constexpr (W == 32) {
+        asm("redux.sync.max.NaN.f32 %0, %0, 0xffffffff;" : "+f"(m));
+        return m;
+    }
 #pragma unroll
     for (int o = W / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
 }
+// Both sums in one chain: even lanes go on with z, odd lanes with t.
 template <int W>
 __device__ __forceinline__ void lanes_sum(float &z, float &t) {
+    const bool odd = (threadIdx.x & 1) != 0;
+    float v = odd ? t : z;
+    const float w = odd ? z : t;
+    v += __shfl_xor_sync(0xffffffffu, w, 1);
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) {
-        z += __shfl_xor_sync(0xffffffffu, z, o);
-        t += __shfl_xor_sync(0xffffffffu, t, o);
-    }
+    for (int o = W / 2; o > 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const float u = __shfl_xor_sync(0xffffffffu, v, 1);
+    z = odd ? u : v;
+    t = odd ? v : u;
 }
 
 // The group's sums from those of its threads: s.m is the maximum of this warp's part of the
 // group already, s.z and s.t this thread's sums against it.  For a group of several warps,
-// one barrier; lane l then holds warp l's sums.
+// one barrier of the block; lane l then holds the sums of the group's warp l.
 template <int TPR>
-__device__ __forceinline__ Soft join_group(Soft s, float scale2, Soft (*red)[kThreads / 32], int slot) {
+__device__ __forceinline__ Soft join_group(Soft s, float scale2, Soft (*red)[kThreads / 32],
+                                           int slot) {
     lanes_sum<(TPR < 32 ? TPR : 32)>(s.z, s.t);
     if constexpr (TPR > 32) {
-        static_assert(TPR == kThreads, "one row a block");
-        constexpr int W = kThreads / 32;
-        if ((threadIdx.x & 31) == 0) red[slot][threadIdx.x >> 5] = s;
+        constexpr int W = TPR / 32;
+        const int warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) == 0) red[slot][warp] = s;
         __syncthreads();
-        s = red[slot][threadIdx.x & (W - 1)];
+        s = red[slot][warp / W * W + (threadIdx.x & (W - 1))];
         const float m = lanes_max<W>(s.m);
         const float c = exp2_fast(scale2 * (s.m - soft_base(m)));
         s.z *= c;
@@ -175,65 +187,188 @@ __device__ __forceinline__ void finish_block(const LossArgs &a, const LossScales
     }
 }
 
-// f of the thread's columns j .. j + V - 1
-template <int V>
-__device__ __forceinline__ void load_shares(const LossArgs &a, const LossScales &c, int j,
-                                            float (&f)[V]) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) f[k] = 0.f;
-    if (j >= a.K) return;
-    int32_t q[V];
-    bool done = false;
-    if constexpr (V % 4 == 0) {
-        if (a.cvec) {
-#pragma unroll
-            for (int k = 0; k < V; k += 4) {
-                const int4 u = *reinterpret_cast<const int4 *>(a.counts + j + k);
-                q[k] = u.x;
-                q[k + 1] = u.y;
-                q[k + 2] = u.z;
-                q[k + 3] = u.w;
-            }
-            done = true;
-        }
-    }
-    if (!done) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) q[k] = a.counts[j + k];
-    }
-#pragma unroll
-    for (int k = 0; k < V; ++k) f[k] = static_cast<float>(q[k]) * c.unit;
+// max of pairs of scores that keeps a NaN (of bf16, before they are widened)
+__device__ __forceinline__ float vec_max(const uint4 *u, int n, float) {
+    float m = -INFINITY;
+    for (int i = 0; i < n; ++i)
+        m = max_nan(max_nan(max_nan(m, __uint_as_float(u[i].x)), __uint_as_float(u[i].y)),
+                    max_nan(__uint_as_float(u[i].z), __uint_as_float(u[i].w)));
+    return m;
+}
+__device__ __forceinline__ uint32_t max_pairs(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float vec_max(const uint4 *u, int n, uint16_t) {
+    uint32_t m = 0xff80ff80u;
+    for (int i = 0; i < n; ++i)
+        m = max_pairs(max_pairs(max_pairs(m, u[i].x), u[i].y), max_pairs(u[i].z, u[i].w));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
 }
 
-// Up to 16 columns a thread, f stays in registers for all rows of the block.
-template <typename T, int V, int NV, int TPR>
-__global__ void __launch_bounds__(kThreads, NV * V <= 8 ? 4 : (NV * V <= 16 ? 3 : 2))
-    balance_loss_kernel(const T *S, T *dS, const LossArgs a) {
+// Rows in 16-byte vectors.  The G rows a block takes at once lie one behind the other: one bulk
+// copy brings them into a ring of `stages` slots, several turns ahead.  f is kept in shared
+// memory.  The arithmetic is nearly as long as the memory access, so two columns go in one
+// instruction where there is one, and an exponent is one multiply-add (scale2 s - scale2 m)
+// unless scale2 m would overflow.
+template <typename T, int NV, int TPR>
+__global__ void __launch_bounds__(kThreads, 2)
+    balance_ring_kernel(const T *S, T *dS, const LossArgs a, int stages,
+                        uint32_t *__restrict__ err, uint64_t wait_ns) {
+    constexpr int V = kVec<T>, H = V / 2, G = kThreads / TPR;
+    __shared__ Soft red[2][kThreads / 32];
+    __shared__ double sums[kThreads];
+    __shared__ uint64_t full[kMaxStages];
+    __shared__ uint32_t abort_flag;
+    extern __shared__ __align__(128) uint8_t space[];
+    float *f = reinterpret_cast<float *>(space);
+    uint8_t *ring = space + (a.K * 4 + 127) / 128 * 128;
+    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) ptx::mbar_init(&full[s], 1);
+        abort_flag = 0u;
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t row_bytes = static_cast<uint32_t>(a.K * sizeof(T));
+    const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * G;
+    auto bring = [&](int64_t i0, int s) {
+        if (i0 >= a.N) return;
+        const uint32_t bytes = static_cast<uint32_t>(a.N - i0 < G ? a.N - i0 : G) * row_bytes;
+        ptx::mbar_arrive_expect_tx(&full[s], bytes);
+        ptx::bulk_load(ring + static_cast<size_t>(s) * G * row_bytes, S + i0 * a.K, bytes,
+                       &full[s]);
+    };
+    if (threadIdx.x == 0)
+        for (int s = 0; s < stages; ++s) bring(first + s * step, s);
+    const LossScales c(a);
+    for (int k = threadIdx.x; k < a.K; k += kThreads)
+        f[k] = static_cast<float>(a.counts[k]) * c.unit;
+    __syncthreads();
+    const float scale2 = a.scale * 1.44269504f;
+    const F2 scale22 = f2(scale2, scale2);
+    double total = 0.0;
+    int slot = 0, stage = 0;
+    uint32_t phase = 0;
+    int64_t i = first + grp;
+    bool keep = i < a.N && row_selects(a, i);
+    T *out = dS + i * a.K + t * V;
+    for (int64_t i0 = first; i0 < a.N; i0 += step, i += step, out += step * a.K) {
+        const bool on = keep;
+        keep = i + step < a.N && row_selects(a, i + step);
+        // a wait that runs out is recorded, and the pass runs to its end without its data
+        if (!ptx::mbar_wait(&full[stage], phase, &abort_flag, wait_ns)) {
+            *const_cast<volatile uint32_t *>(&abort_flag) = 1u;
+            err[0] = kErrTimeout;
+        }
+        const uint8_t *x = ring + (static_cast<size_t>(stage) * G + grp) * row_bytes + t * 16;
+        uint4 u[NV];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            Raw<T, V> r;
+            r.lowest();
+            if (on && (n * TPR + t) * V < a.K)
+                r.u = *reinterpret_cast<const uint4 *>(x + n * TPR * 16);
+            u[n] = r.u;
+        }
+        const float m = lanes_max<(TPR < 32 ? TPR : 32)>(vec_max(u, NV, T()));
+        const float base = soft_base(m), base2 = scale2 * base;
+        const bool direct = fabsf(base2) <= 1e37f;
+        const F2 off = f2(-base2, -base2);
+        F2 e[NV][H];
+        F2 z2 = f2(0.f, 0.f), t2 = z2;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            unpack2(u[n], e[n]);
+            const float4 *fp = reinterpret_cast<const float4 *>(f + (n * TPR + t) * V);
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                float lo, hi;
+                if (direct) {
+                    split(fma2(e[n][k], scale22, off), lo, hi);
+                } else {  // (also where base is NaN)
+                    split(e[n][k], lo, hi);
+                    lo = scale2 * (lo - base);
+                    hi = scale2 * (hi - base);
+                }
+                e[n][k] = f2(exp2_fast(lo), exp2_fast(hi));
+                z2 = add2(z2, e[n][k]);
+            }
+            if ((n * TPR + t) * V < a.K) {
+#pragma unroll
+                for (int k = 0; k < H; k += 2) {
+                    const float4 q = fp[k / 2];
+                    t2 = fma2(e[n][k], f2(q.x, q.y), t2);
+                    t2 = fma2(e[n][k + 1], f2(q.z, q.w), t2);
+                }
+            }
+        }
+        const Soft s = join_group<TPR>(Soft{m, sum2(z2), sum2(t2)}, scale2, red, slot);
+        if constexpr (TPR <= 32) __syncthreads();
+        slot ^= 1;
+        // every thread has the slot's rows in registers now
+        if (threadIdx.x == 0) bring(i0 + stages * step, stage);
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+        const float inv = s.m == -INFINITY ? 0.f : rcp_fast(s.z);
+        const float ti = s.t * inv;
+        if (t == 0 && on) total += ti;
+        if (dS == nullptr || i >= a.N) continue;
+        // this warp's exponentials against the group's maximum, over the sum
+        const float gp = TPR > 32 ? c.gc * exp2_fast(scale2 * (m - soft_base(s.m))) * inv
+                                  : c.gc * inv;
+        const F2 gp2 = f2(gp, gp), gt2 = f2(-ti * gp, -ti * gp);
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            if ((n * TPR + t) * V < a.K) {
+                const float4 *fp = reinterpret_cast<const float4 *>(f + (n * TPR + t) * V);
+                F2 v[H];
+#pragma unroll
+                for (int k = 0; k < H; k += 2) {
+                    const float4 q = fp[k / 2];
+                    v[k] = mul2(e[n][k], fma2(f2(q.x, q.y), gp2, gt2));
+                    v[k + 1] = mul2(e[n][k + 1], fma2(f2(q.z, q.w), gp2, gt2));
+                }
+                *reinterpret_cast<uint4 *>(out + n * TPR * V) = pack2(v);
+            }
+        }
+    }
+    finish_block(a, c, total, t == 0, sums);
+    if (abort_flag) {  // give copies already in flight a moment to land (bounded)
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (ptx::globaltimer_ns() - t0 < 200000ull) {
+        }
+    }
+}
+
+// Rows that are not in 16-byte vectors, element by element.
+template <typename T, int NV, int TPR>
+__global__ void __launch_bounds__(kThreads, 2)
+    balance_elements_kernel(const T *S, T *dS, const LossArgs a) {
     __shared__ Soft red[2][kThreads / 32];
     __shared__ double sums[kThreads];
     pdl_wait();
     pdl_trigger();
     constexpr int G = kThreads / TPR;
-    constexpr bool KEEP_F = NV * V <= 16;
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const LossScales c(a);
     const float scale2 = a.scale * 1.44269504f;
     double total = 0.0;
     int slot = 0;
-    Raw<T, V> x[NV];
-    float f[KEEP_F ? NV : 1][V];
-    if constexpr (KEEP_F) {
-#pragma unroll
-        for (int n = 0; n < NV; ++n) load_shares<V>(a, c, (n * TPR + t) * V, f[n]);
-    }
+    T x[NV];
     bool keep = false;
-    // padding rows are read like the others (their values are not used)
     auto fetch = [&](int64_t i) {
         keep = i < a.N && row_selects(a, i);
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int j = (n * TPR + t) * V;
-            if (i < a.N && j < a.K) x[n].load(S + i * a.K + j);
+            head_store(&x[n], -INFINITY);
+            if (keep && n * TPR + t < a.K) x[n] = S[i * a.K + n * TPR + t];
         }
     };
     const int64_t step = static_cast<int64_t>(gridDim.x) * G;
@@ -242,17 +377,12 @@ __global__ void __launch_bounds__(kThreads, NV * V <= 8 ? 4 : (NV * V <= 16 ? 3 
     for (; i0 < a.N; i0 += step) {
         const int64_t i = i0 + grp;
         const bool on = keep;
-        float e[NV][V];
+        float e[NV];
         float m = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const bool in = on && (n * TPR + t) * V < a.K;
-            x[n].get(e[n]);
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                e[n][k] = in ? e[n][k] : -INFINITY;
-                m = max_nan(m, e[n][k]);
-            }
+            e[n] = head_load(&x[n]);
+            m = max_nan(m, e[n]);
         }
         if (i0 + step < a.N) fetch(i0 + step + grp);
         m = lanes_max<(TPR < 32 ? TPR : 32)>(m);
@@ -260,35 +390,25 @@ __global__ void __launch_bounds__(kThreads, NV * V <= 8 ? 4 : (NV * V <= 16 ? 3 
         const float base = soft_base(m);
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            float g[V];
-            if constexpr (!KEEP_F) load_shares<V>(a, c, (n * TPR + t) * V, g);
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                e[n][k] = exp2_fast(scale2 * (e[n][k] - base));
-                s.z += e[n][k];
-                s.t += e[n][k] * (KEEP_F ? f[KEEP_F ? n : 0][k] : g[k]);
-            }
+            const int j = n * TPR + t;
+            e[n] = exp2_fast(scale2 * (e[n] - base));
+            s.z += e[n];
+            if (j < a.K) s.t += e[n] * (static_cast<float>(a.counts[j]) * c.unit);
         }
         s = join_group<TPR>(s, scale2, red, slot);
         slot ^= 1;
-        const float inv = s.m == -INFINITY ? 0.f : 1.f / s.z;
+        const float inv = s.m == -INFINITY ? 0.f : rcp_fast(s.z);
         const float ti = s.t * inv;
         if (t == 0 && on) total += ti;
         if (dS != nullptr && i < a.N) {
-            // this warp's exponentials against the group's maximum, over the sum
-            const float gp = TPR > 32 ? c.gc * exp2_fast(scale2 * (m - soft_base(s.m))) * inv : c.gc * inv;
-            const float gt = -ti * gp;
+            const float gp = TPR > 32 ? c.gc * exp2_fast(scale2 * (m - soft_base(s.m))) * inv
+                                      : c.gc * inv;
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
-                const int j = (n * TPR + t) * V;
-                if (j < a.K) {
-                    float v[V], g[V];
-                    if constexpr (!KEEP_F) load_shares<V>(a, c, j, g);
-#pragma unroll
-                    for (int k = 0; k < V; ++k)
-                        v[k] = e[n][k] * ((KEEP_F ? f[KEEP_F ? n : 0][k] : g[k]) * gp + gt);
-                    Raw<T, V>::put(dS + i * a.K + j, v);
-                }
+                const int j = n * TPR + t;
+                if (j < a.K)
+                    head_store(dS + i * a.K + j,
+                               e[n] * (static_cast<float>(a.counts[j]) * c.unit * gp - ti * gp));
             }
         }
     }
@@ -358,41 +478,75 @@ __global__ void balance_join_kernel(const double *__restrict__ part, int parts, 
     }
 }
 
-template <typename T, int V, int NV, int TPR>
-cudaError_t loss_cfg(const BalanceArgs &b, const LossArgs &a, int *grid, cudaStream_t st) {
-    const int64_t g = ceil_div(a.N, kThreads / TPR);
-    *grid = static_cast<int>(g < b.parts ? g : b.parts);
-    return launch_pdl(balance_loss_kernel<T, V, NV, TPR>, dim3(*grid), dim3(kThreads), 0, st,
-                      static_cast<const T *>(b.S), static_cast<T *>(b.dS), a);
+int loss_grid(const BalanceArgs &b, int groups) {
+    const int64_t g = ceil_div(b.N, groups);
+    return static_cast<int>(g < b.parts ? g : b.parts);
 }
 
-// About 16 columns a thread; from 32 a thread in a block on, rows are read twice.
-template <typename T, int V>
-cudaError_t loss_v(const BalanceArgs &b, const LossArgs &a, int *grid, cudaStream_t st) {
-    constexpr int C16 = 16 / V;
-    if (a.K <= 8 * V) return loss_cfg<T, V, 1, 8>(b, a, grid, st);
-    if (a.K <= 16 * V) return loss_cfg<T, V, 1, 16>(b, a, grid, st);
-    if (a.K <= 32 * V) return loss_cfg<T, V, 1, 32>(b, a, grid, st);
-    if (a.K <= 32 * 16) return loss_cfg<T, V, C16, 32>(b, a, grid, st);
-    if (a.K <= 32 * 32) return loss_cfg<T, V, 2 * C16, 32>(b, a, grid, st);
-    if (a.K <= kThreads * 16) return loss_cfg<T, V, C16, kThreads>(b, a, grid, st);
-    if (a.K <= kThreads * 32) return loss_cfg<T, V, 2 * C16, kThreads>(b, a, grid, st);
-    *grid = static_cast<int>(a.N < b.parts ? a.N : b.parts);
-    return launch_pdl(balance_long_kernel<T>, dim3(*grid), dim3(kThreads), 0, st,
+template <typename T, int NV, int TPR>
+cudaError_t loss_ring(const BalanceArgs &b, const LossArgs &a, int *grid, cudaStream_t st) {
+    auto kernel = balance_ring_kernel<T, NV, TPR>;
+    const int slot = kThreads / TPR * a.K * static_cast<int>(sizeof(T));
+    int stages = kRingBytes / slot;
+    if (stages < 2) stages = 2;
+    if (stages > kMaxStages) stages = kMaxStages;
+    static std::atomic<uint64_t> smem_set{0};
+    const cudaError_t e = smem_opt_in(kernel, 128 << 10, smem_set);
+    if (e != cudaSuccess) return e;
+    *grid = loss_grid(b, kThreads / TPR);
+    return launch_pdl(kernel, dim3(*grid), dim3(kThreads),
+                      round_up(a.K * 4, 128) + static_cast<size_t>(stages) * slot, st,
+                      static_cast<const T *>(b.S), static_cast<T *>(b.dS), a, stages, b.err,
+                      kDefaultWaitNs);
+}
+
+template <typename T, int NV, int TPR>
+cudaError_t loss_elements(const BalanceArgs &b, const LossArgs &a, int *grid, cudaStream_t st) {
+    *grid = loss_grid(b, kThreads / TPR);
+    return launch_pdl(balance_elements_kernel<T, NV, TPR>, dim3(*grid), dim3(kThreads), 0, st,
                       static_cast<const T *>(b.S), static_cast<T *>(b.dS), a);
 }
 
 template <typename T>
+cudaError_t loss_long(const BalanceArgs &b, const LossArgs &a, int *grid, cudaStream_t st) {
+    *grid = loss_grid(b, 1);
+    return launch_pdl(balance_long_kernel<T>, dim3(*grid), dim3(kThreads), 0, st,
+                      static_cast<const T *>(b.S), static_cast<T *>(b.dS), a);
+}
+
+// Up to 32 columns a thread (16 for one element at a time), and as few threads a row as that
+// allows: the sums over the threads cost about as much as ten columns.
+template <typename T>
 cudaError_t loss_t(const BalanceArgs &b, const LossArgs &a, int *grid, cudaStream_t st) {
-    const bool vec = a.K % kVec<T> == 0 && aligned(b.S, 16) && aligned(b.dS, 16);
-    return vec ? loss_v<T, kVec<T>>(b, a, grid, st) : loss_v<T, 1>(b, a, grid, st);
+    constexpr int V = kVec<T>, C32 = 32 / V;
+    const int K = a.K;
+    if (K % V == 0 && aligned(b.S, 16) && aligned(b.dS, 16)) {
+        if (K <= 8 * V) return loss_ring<T, 1, 8>(b, a, grid, st);
+        if (K <= 16 * V) return loss_ring<T, 1, 16>(b, a, grid, st);
+        if (K <= 32 * V) return loss_ring<T, 1, 32>(b, a, grid, st);
+        if (K <= 32 * 16) return loss_ring<T, C32 / 2, 32>(b, a, grid, st);
+        if (K <= 32 * 32) return loss_ring<T, C32, 32>(b, a, grid, st);
+        if (K <= 64 * 32) return loss_ring<T, C32, 64>(b, a, grid, st);
+        if (K <= 128 * 32) return loss_ring<T, C32, 128>(b, a, grid, st);
+        if (K <= 256 * 32) return loss_ring<T, C32, 256>(b, a, grid, st);
+        return loss_long<T>(b, a, grid, st);
+    }
+    if (K <= 8) return loss_elements<T, 1, 8>(b, a, grid, st);
+    if (K <= 32) return loss_elements<T, 1, 32>(b, a, grid, st);
+    if (K <= 32 * 4) return loss_elements<T, 4, 32>(b, a, grid, st);
+    if (K <= 32 * 16) return loss_elements<T, 16, 32>(b, a, grid, st);
+    if (K <= 64 * 16) return loss_elements<T, 16, 64>(b, a, grid, st);
+    if (K <= 256 * 8) return loss_elements<T, 8, 256>(b, a, grid, st);
+    if (K <= 256 * 16) return loss_elements<T, 16, 256>(b, a, grid, st);
+    if (K <= 256 * 32) return loss_elements<T, 32, 256>(b, a, grid, st);
+    return loss_long<T>(b, a, grid, st);
 }
 
 }  // namespace
 
 int64_t balance_parts(int64_t N, int K) {
     (void)K;
-    return N < 1 ? 1 : (N < 148 * 8 ? N : 148 * 8);
+    return N < 1 ? 1 : (N < 148 * 3 ? N : 148 * 3);
 }
 
 cudaError_t launch_balance_counts(const int32_t *labels, int64_t N, int top, int K,
@@ -429,7 +583,6 @@ cudaError_t launch_balance_loss(const BalanceArgs &b, cudaStream_t st) {
     a.rows = b.rows;
     a.scale = b.scale;
     a.coef = b.coef;
-    a.cvec = aligned(b.counts, 16);
     a.loss = b.loss;
     a.part = b.part;
     int grid = 0;

@@ -141,6 +141,7 @@ FK_API fk_status fk_layer_norm_backward(const void *dY, const void *X, fk_dtype 
     a.dbeta = dbeta;
     a.part = ws_ptr<float>(ws, 256);
     a.parts = layer_norm_parts(N, d);
+    a.err = ws_ptr<uint32_t>(ws, 0);
     return done(launch_layer_norm_backward(a, stream));
 }
 
@@ -287,6 +288,7 @@ FK_API fk_status fk_balance_loss(const void *S, fk_dtype dtype, int64_t N, int K
     a.dS = dS;
     a.part = ws_ptr<double>(ws, 256);
     a.parts = balance_parts(N, K);
+    a.err = ws_ptr<uint32_t>(ws, 0);
     return done(launch_balance_loss(a, stream));
 }
 

@@ -64,6 +64,10 @@ struct Raw<T, kVec<T>> {
     uint4 u;
     __device__ __forceinline__ void load(const T *p) { u = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void lowest() {  // -inf
+        const uint32_t w = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+        u = make_uint4(w, w, w, w);
+    }
     __device__ __forceinline__ void get(float (&v)[kVec<T>]) const { unpack16(u, v); }
     static __device__ __forceinline__ void put(T *p, const float (&v)[kVec<T>]) {
         *reinterpret_cast<uint4 *>(p) = pack16(v);
@@ -110,6 +114,7 @@ struct Raw<T, 1> {
     T u;
     __device__ __forceinline__ void load(const T *p) { u = *p; }
     __device__ __forceinline__ void zero() { u = T(0); }
+    __device__ __forceinline__ void lowest() { head_store(&u, -INFINITY); }
     __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = head_load(&u); }
     static __device__ __forceinline__ void put(T *p, const float (&v)[1]) { head_store(p, v[0]); }
 };
@@ -134,6 +139,67 @@ __device__ __forceinline__ void load_params(const float *p, int vec, float (&v)[
     for (int j = 0; j < V; ++j) v[j] = p[j];
 }
 
+// Two fp32 operations an instruction.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(F2 a, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ float sum2(F2 a) {
+    float lo, hi;
+    split(a, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+// 16 bytes of points as pairs.
+__device__ __forceinline__ void unpack2(const uint4 &u, F2 (&v)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack2(const uint4 &u, F2 (&v)[2]) {
+    v[0] = f2(__uint_as_float(u.x), __uint_as_float(u.y));
+    v[1] = f2(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+__device__ __forceinline__ uint4 pack2(const F2 (&v)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        split(v[i], lo, hi);
+        w[i] = pack_bf16(lo, hi);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 pack2(const F2 (&v)[2]) {
+    float a, b, c, d;
+    split(v[0], a, b);
+    split(v[1], c, d);
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c),
+                      __float_as_uint(d));
+}
+
 // ----------------------------------------------------------------- layer norm
 struct LayerNormArgs {
     const void *X, *dY;
@@ -147,6 +213,7 @@ struct LayerNormArgs {
     float *dgamma, *dbeta;  // backward, optional
     float *part;            // backward: [parts][2][d] partial column sums
     int64_t parts;
+    uint32_t *err;          // backward: the workspace's error word
 };
 // Row groups whose column sums of the backward pass are formed apart and then joined in
 // order (the workspace holds two rows of d floats for each).
@@ -168,6 +235,7 @@ struct BalanceArgs {
     void *dS;  // optional
     double *part;
     int64_t parts;
+    uint32_t *err;  // the workspace's error word
 };
 int64_t balance_parts(int64_t N, int K);
 cudaError_t launch_balance_counts(const int32_t *labels, int64_t N, int top, int K,

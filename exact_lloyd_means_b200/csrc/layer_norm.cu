@@ -11,14 +11,18 @@
 // where rows are not multiples of 16 bytes); statistics are sums over the group.  Rows that
 // do not fit the registers of a block are read again for each sum.
 #include "head.cuh"
+#include "ptx_sm100.cuh"
 
 namespace fk {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxStages = 8;   // slots of the backward pass's ring of rows
+constexpr int kRingBytes = 96 << 10;  // its size: two blocks an SM
 
-// Sum of v over the TPR threads of a row group; red: a block's scratch, [2][warps][2], one of
-// whose halves (`slot`) this row uses, so that one barrier a row is enough.
+// Sums of a and b over the TPR threads of a row group; red: a block's scratch, of which `slot`
+// picks the half this row uses, so that one barrier a row is enough (every group of the block
+// takes part in it).
 template <int TPR>
 __device__ __forceinline__ void group_sum2(float &a, float &b, float (*red)[kThreads / 32][2],
                                            int slot) {
@@ -28,7 +32,7 @@ __device__ __forceinline__ void group_sum2(float &a, float &b, float (*red)[kThr
         b += __shfl_xor_sync(0xffffffffu, b, o);
     }
     if constexpr (TPR > 32) {
-        static_assert(TPR == kThreads, "one row a block");
+        constexpr int W = TPR / 32;
         const int warp = threadIdx.x >> 5;
         if ((threadIdx.x & 31) == 0) {
             red[slot][warp][0] = a;
@@ -37,9 +41,9 @@ __device__ __forceinline__ void group_sum2(float &a, float &b, float (*red)[kThr
         __syncthreads();
         a = b = 0.f;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            a += red[slot][w][0];
-            b += red[slot][w][1];
+        for (int w = 0; w < W; ++w) {
+            a += red[slot][warp / W * W + w][0];
+            b += red[slot][warp / W * W + w][1];
         }
     }
 }
@@ -151,93 +155,12 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// Backward: dX row by row, and the block's column sums of its rows in registers; the groups
-// of a block are joined in shared memory, the blocks by layer_norm_join_kernel.  The next
-// row is loaded before this row's sums are formed.
-template <typename T, int V, int NV, int TPR>
-__global__ void __launch_bounds__(kThreads)
-    layer_norm_backward_kernel(const T *dY, const T *__restrict__ X, int64_t N, int d,
-                               const float *__restrict__ gamma, int pvec,
-                               const float *__restrict__ mean, const float *__restrict__ rstd,
-                               T *dX, float *__restrict__ part) {
+// The block's column sums, joined over its row groups in shared memory.
+template <int V, int NV, int TPR>
+__device__ __forceinline__ void write_part(const float (&sg)[NV][V], const float (&sb)[NV][V],
+                                           int d, float *sums, float *part) {
     constexpr int G = kThreads / TPR;
-    __shared__ float red[2][kThreads / 32][2];
-    __shared__ float sums[G > 1 ? kThreads * 2 : 2];
-    pdl_wait();
-    pdl_trigger();
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-    const float inv = 1.f / static_cast<float>(d);
-    float sg[NV][V], sb[NV][V];
-#pragma unroll
-    for (int n = 0; n < NV; ++n)
-#pragma unroll
-        for (int k = 0; k < V; ++k) sg[n][k] = sb[n][k] = 0.f;
-    Raw<T, V> x[NV], y[NV];
-    float mu = 0.f, r = 0.f;
-    auto fetch = [&](int64_t i) {
-        if (i < N) {
-            mu = mean[i];
-            r = rstd[i];
-        }
-#pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const int j = (n * TPR + t) * V;
-            if (i < N && j < d) {
-                x[n].load(X + i * d + j);
-                y[n].load(dY + i * d + j);
-            } else {
-                x[n].zero();
-                y[n].zero();
-            }
-        }
-    };
-    const int64_t step = static_cast<int64_t>(gridDim.x) * G;
-    int64_t i0 = static_cast<int64_t>(blockIdx.x) * G;
-    if (i0 < N) fetch(i0 + grp);
-    int slot = 0;
-    for (; i0 < N; i0 += step) {
-        const int64_t i = i0 + grp;
-        float h[NV][V], w[NV][V];
-        float a = 0.f, b = 0.f;
-        const float rr = r;
-#pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const int j = (n * TPR + t) * V;
-            float xv[V], yv[V], g[V];
-            x[n].get(xv);
-            y[n].get(yv);
-#pragma unroll
-            for (int k = 0; k < V; ++k) g[k] = 1.f;
-            if (gamma && j < d) load_params<V>(gamma + j, pvec, g);
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                h[n][k] = j < d && i < N ? (xv[k] - mu) * r : 0.f;
-                w[n][k] = yv[k] * g[k];
-                a += w[n][k];
-                b += w[n][k] * h[n][k];
-                sg[n][k] += yv[k] * h[n][k];
-                sb[n][k] += yv[k];
-            }
-        }
-        if (i0 + step < N) fetch(i0 + step + grp);
-        group_sum2<TPR>(a, b, red, slot);
-        slot ^= 1;
-        a *= inv;
-        b *= inv;
-        if (dX != nullptr && i < N) {
-#pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                const int j = (n * TPR + t) * V;
-                if (j < d) {
-                    float v[V];
-#pragma unroll
-                    for (int k = 0; k < V; ++k) v[k] = rr * (w[n][k] - a - h[n][k] * b);
-                    Raw<T, V>::put(dX + i * d + j, v);
-                }
-            }
-        }
-    }
-    if (part == nullptr) return;
     float *out = part + static_cast<int64_t>(blockIdx.x) * 2 * d;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
@@ -263,6 +186,222 @@ __global__ void __launch_bounds__(kThreads)
             }
         }
     }
+}
+
+// Backward, rows in 16-byte vectors: dX row by row, and the block's column sums of its rows in
+// registers; the groups of a block are joined in shared memory, the blocks by
+// layer_norm_join_kernel.  The G rows a block takes at once lie one behind the other, so one
+// bulk copy a tensor brings them into a ring of `stages` slots, several turns ahead: with the
+// sums in registers there is no room there for enough loads in flight.
+template <typename T, int NV, int TPR>
+__global__ void __launch_bounds__(kThreads)
+    layer_norm_backward_ring_kernel(const T *dY, const T *__restrict__ X, int64_t N, int d,
+                                    const float *__restrict__ gamma, int pvec,
+                                    const float *__restrict__ mean,
+                                    const float *__restrict__ rstd, T *dX,
+                                    float *__restrict__ part, int stages,
+                                    uint32_t *__restrict__ err, uint64_t wait_ns) {
+    constexpr int V = kVec<T>, H = V / 2, G = kThreads / TPR;
+    __shared__ float red[2][kThreads / 32][2];
+    __shared__ float sums[G > 1 ? kThreads * 2 : 2];
+    __shared__ uint64_t full[kMaxStages];
+    __shared__ uint32_t abort_flag;
+    extern __shared__ __align__(128) uint8_t ring[];
+    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) ptx::mbar_init(&full[s], 1);
+        abort_flag = 0u;
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t row_bytes = static_cast<uint32_t>(d * sizeof(T));
+    const uint32_t half = G * row_bytes;  // a slot: G rows of X, then G rows of dY
+    const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * G;
+    auto bring = [&](int64_t i0, int s) {
+        if (i0 >= N) return;
+        const uint32_t rows = static_cast<uint32_t>(N - i0 < G ? N - i0 : G);
+        ptx::mbar_arrive_expect_tx(&full[s], 2 * rows * row_bytes);
+        uint8_t *p = ring + static_cast<size_t>(s) * 2 * half;
+        ptx::bulk_load(p, X + i0 * d, rows * row_bytes, &full[s]);
+        ptx::bulk_load(p + half, dY + i0 * d, rows * row_bytes, &full[s]);
+    };
+    if (threadIdx.x == 0)
+        for (int s = 0; s < stages; ++s) bring(first + s * step, s);
+    F2 sg[NV][H], sb[NV][H], gm[NV][H];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int j = (n * TPR + t) * V;
+        float g[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) g[k] = j < d ? 1.f : 0.f;
+        if (gamma && j < d) load_params<V>(gamma + j, pvec, g);
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            sg[n][k] = sb[n][k] = f2(0.f, 0.f);
+            gm[n][k] = f2(g[2 * k], g[2 * k + 1]);
+        }
+    }
+    const float inv = 1.f / static_cast<float>(d);
+    float mu1 = 0.f, r1 = 0.f;  // of the next row
+    if (first + grp < N) {
+        mu1 = mean[first + grp];
+        r1 = rstd[first + grp];
+    }
+    int slot = 0, s = 0;
+    uint32_t phase = 0;
+    for (int64_t i0 = first; i0 < N; i0 += step) {
+        const int64_t i = i0 + grp;
+        const bool row = i < N;
+        const float mu = mu1, r = r1;
+        if (i + step < N) {
+            mu1 = mean[i + step];
+            r1 = rstd[i + step];
+        }
+        // a wait that runs out is recorded, and the pass runs to its end without its data
+        if (!ptx::mbar_wait(&full[s], phase, &abort_flag, wait_ns)) {
+            *const_cast<volatile uint32_t *>(&abort_flag) = 1u;
+            err[0] = kErrTimeout;
+        }
+        const T *x = reinterpret_cast<const T *>(ring + static_cast<size_t>(s) * 2 * half +
+                                                 grp * row_bytes);
+        const T *y = reinterpret_cast<const T *>(reinterpret_cast<const uint8_t *>(x) + half);
+        F2 h[NV][H], w[NV][H];
+        F2 a2 = f2(0.f, 0.f), b2 = a2;
+        const F2 rr = f2(r, r), off = f2(-mu, -mu);
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int j = (n * TPR + t) * V;
+            F2 yv[H];
+            uint4 ux = make_uint4(0u, 0u, 0u, 0u), uy = ux;
+            if (row && j < d) {
+                ux = *reinterpret_cast<const uint4 *>(x + j);
+                uy = *reinterpret_cast<const uint4 *>(y + j);
+            }
+            unpack2(ux, h[n]);
+            unpack2(uy, yv);  // (nothing where there is no column or no row)
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                h[n][k] = mul2(add2(h[n][k], off), rr);  // (x r - mu r would cancel)
+                w[n][k] = mul2(yv[k], gm[n][k]);
+                a2 = add2(a2, w[n][k]);
+                b2 = fma2(w[n][k], h[n][k], b2);
+                sg[n][k] = fma2(yv[k], h[n][k], sg[n][k]);
+                sb[n][k] = add2(sb[n][k], yv[k]);
+            }
+        }
+        float a = sum2(a2), b = sum2(b2);
+        group_sum2<TPR>(a, b, red, slot);
+        if constexpr (TPR <= 32) __syncthreads();
+        slot ^= 1;
+        // every thread has the slot's rows in registers now
+        if (threadIdx.x == 0) bring(i0 + stages * step, s);
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+        }
+        if (dX != nullptr && row) {
+            const float ra = -r * a * inv, rb = -r * b * inv;
+            const F2 ra2 = f2(ra, ra), rb2 = f2(rb, rb);
+            T *o = dX + i * d + t * V;
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                if ((n * TPR + t) * V < d) {
+                    F2 v[H];
+#pragma unroll
+                    for (int k = 0; k < H; ++k)
+                        v[k] = fma2(rr, w[n][k], fma2(rb2, h[n][k], ra2));
+                    *reinterpret_cast<uint4 *>(o + n * TPR * V) = pack2(v);
+                }
+            }
+        }
+    }
+    if (part != nullptr) {
+        float g[NV][V], b[NV][V];
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                split(sg[n][k], g[n][2 * k], g[n][2 * k + 1]);
+                split(sb[n][k], b[n][2 * k], b[n][2 * k + 1]);
+            }
+        write_part<V, NV, TPR>(g, b, d, sums, part);
+    }
+    if (abort_flag) {  // give copies already in flight a moment to land (bounded)
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (ptx::globaltimer_ns() - t0 < 200000ull) {
+        }
+    }
+}
+
+// The same for rows that are not in 16-byte vectors, element by element; the next row is
+// loaded before this row's sums are formed.
+template <typename T, int NV, int TPR>
+__global__ void __launch_bounds__(kThreads)
+    layer_norm_backward_kernel(const T *dY, const T *__restrict__ X, int64_t N, int d,
+                               const float *__restrict__ gamma, const float *__restrict__ mean,
+                               const float *__restrict__ rstd, T *dX, float *__restrict__ part) {
+    constexpr int G = kThreads / TPR;
+    __shared__ float red[2][kThreads / 32][2];
+    __shared__ float sums[G > 1 ? kThreads * 2 : 2];
+    pdl_wait();
+    pdl_trigger();
+    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    const float inv = 1.f / static_cast<float>(d);
+    float sg[NV][1], sb[NV][1];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) sg[n][0] = sb[n][0] = 0.f;
+    T x[NV], y[NV];
+    float mu = 0.f, r = 0.f;
+    auto fetch = [&](int64_t i) {
+        if (i < N) {
+            mu = mean[i];
+            r = rstd[i];
+        }
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int j = n * TPR + t;
+            const bool in = i < N && j < d;
+            x[n] = in ? X[i * d + j] : T(0);
+            y[n] = in ? dY[i * d + j] : T(0);
+        }
+    };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+    int64_t i0 = static_cast<int64_t>(blockIdx.x) * G;
+    if (i0 < N) fetch(i0 + grp);
+    int slot = 0;
+    for (; i0 < N; i0 += step) {
+        const int64_t i = i0 + grp;
+        float h[NV], w[NV];
+        float a = 0.f, b = 0.f;
+        const float rr = r;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int j = n * TPR + t;
+            const bool in = j < d && i < N;
+            const float yv = head_load(&y[n]);
+            h[n] = in ? (head_load(&x[n]) - mu) * r : 0.f;
+            w[n] = in && gamma ? yv * gamma[j] : yv;
+            a += w[n];
+            b += w[n] * h[n];
+            sg[n][0] += yv * h[n];
+            sb[n][0] += yv;
+        }
+        if (i0 + step < N) fetch(i0 + step + grp);
+        group_sum2<TPR>(a, b, red, slot);
+        slot ^= 1;
+        if (dX != nullptr && i < N) {
+            const float ra = -rr * a * inv, rb = -rr * b * inv;
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                const int j = n * TPR + t;
+                if (j < d) head_store(dX + i * d + j, rr * w[n] + (rb * h[n] + ra));
+            }
+        }
+    }
+    if (part != nullptr) write_part<1, NV, TPR>(sg, sb, d, sums, part);
 }
 
 // The same for rows longer than a block's registers: dX, one block a row ...
@@ -318,26 +457,28 @@ __global__ void __launch_bounds__(128)
 }
 
 // dgamma and dbeta: the sums of the parts.  32 columns a block (of 2 d: dgamma's, then
-// dbeta's), 8 runs of parts side by side.
-__global__ void __launch_bounds__(kThreads)
+// dbeta's), 32 runs of parts side by side.
+__global__ void __launch_bounds__(1024)
     layer_norm_join_kernel(const float *__restrict__ part, int parts, int64_t d,
                            float *__restrict__ dgamma, float *__restrict__ dbeta) {
-    __shared__ float red[8][33];
+    __shared__ float red[32][33];
     pdl_wait();
     pdl_trigger();
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + x;
     float s = 0.f;
     if (c < 2 * d) {
-#pragma unroll 4
-        for (int p = y; p < parts; p += 8) s += part[static_cast<int64_t>(p) * 2 * d + c];
+#pragma unroll 8
+        for (int p = y; p < parts; p += 32) s += part[static_cast<int64_t>(p) * 2 * d + c];
     }
     red[y][x] = s;
     __syncthreads();
-    if (y == 0 && c < 2 * d) {
-        for (int t = 1; t < 8; ++t) s += red[t][x];
-        float *o = c < d ? dgamma : dbeta;
-        if (o) o[c < d ? c : c - d] = s;
+    // warp y sums the runs of column y
+    s = warp_sum_f(red[x][y]);
+    const int64_t o = static_cast<int64_t>(blockIdx.x) * 32 + y;
+    if (x == 0 && o < 2 * d) {
+        float *out = o < d ? dgamma : dbeta;
+        if (out) out[o < d ? o : o - d] = s;
     }
 }
 
@@ -347,8 +488,8 @@ int block_grid(int64_t rows, int groups, int per_sm) {
     return static_cast<int>(g < cap ? g : cap);
 }
 
-// Blocks of the backward pass, and so parts of the column sums: at most four an SM.
-constexpr int64_t kMaxParts = 148 * 4;
+// Blocks of the backward pass, and so parts of the column sums: at most two an SM.
+constexpr int64_t kMaxParts = 148 * 2;
 
 template <typename T, int V, int NV, int TPR>
 cudaError_t forward_cfg(const LayerNormArgs &a, cudaStream_t st) {
@@ -381,16 +522,39 @@ cudaError_t forward_v(const LayerNormArgs &a, cudaStream_t st) {
     return e;
 }
 
-template <typename T, int V, int NV, int TPR>
-cudaError_t backward_cfg(const LayerNormArgs &a, cudaStream_t st, int *parts) {
-    const int64_t g = ceil_div(a.N, kThreads / TPR);
-    *parts = static_cast<int>(g < a.parts ? g : a.parts);
+int backward_grid(const LayerNormArgs &a, int groups) {
+    const int64_t g = ceil_div(a.N, groups);
+    return static_cast<int>(g < a.parts ? g : a.parts);
+}
+
+template <typename T, int NV, int TPR>
+cudaError_t backward_ring(const LayerNormArgs &a, cudaStream_t st, int *parts) {
+    auto kernel = layer_norm_backward_ring_kernel<T, NV, TPR>;
+    const int slot = 2 * (kThreads / TPR) * a.d * static_cast<int>(sizeof(T));
+    int stages = kRingBytes / slot;
+    if (stages < 2) stages = 2;
+    if (stages > kMaxStages) stages = kMaxStages;
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = smem_opt_in(kernel, 160 << 10, smem_set);
+    if (e != cudaSuccess) return e;
+    *parts = backward_grid(a, kThreads / TPR);
+    e = launch_pdl(kernel, dim3(*parts), dim3(kThreads), static_cast<size_t>(stages) * slot, st,
+                   static_cast<const T *>(a.dY), static_cast<const T *>(a.X), a.N, a.d, a.gamma,
+                   static_cast<int>(aligned(a.gamma, 16)), static_cast<const float *>(a.mean),
+                   static_cast<const float *>(a.rstd), static_cast<T *>(a.Y),
+                   a.dgamma || a.dbeta ? a.part : nullptr, stages, a.err, kDefaultWaitNs);
+    if (e == cudaSuccess) note_launch();
+    return e;
+}
+
+template <typename T, int NV, int TPR>
+cudaError_t backward_elements(const LayerNormArgs &a, cudaStream_t st, int *parts) {
+    *parts = backward_grid(a, kThreads / TPR);
     const cudaError_t e = launch_pdl(
-        layer_norm_backward_kernel<T, V, NV, TPR>, dim3(*parts), dim3(kThreads), 0, st,
+        layer_norm_backward_kernel<T, NV, TPR>, dim3(*parts), dim3(kThreads), 0, st,
         static_cast<const T *>(a.dY), static_cast<const T *>(a.X), a.N, a.d, a.gamma,
-        static_cast<int>(aligned(a.gamma, 16)), static_cast<const float *>(a.mean),
-        static_cast<const float *>(a.rstd), static_cast<T *>(a.Y),
-        a.dgamma || a.dbeta ? a.part : nullptr);
+        static_cast<const float *>(a.mean), static_cast<const float *>(a.rstd),
+        static_cast<T *>(a.Y), a.dgamma || a.dbeta ? a.part : nullptr);
     if (e == cudaSuccess) note_launch();
     return e;
 }
@@ -420,17 +584,31 @@ cudaError_t backward_long(const LayerNormArgs &a, cudaStream_t st, int *parts) {
     return e;
 }
 
-// At most 16 columns a thread up to a block a row, then 32 (their sums take two registers
-// each).
-template <typename T, int V>
-cudaError_t backward_v(const LayerNormArgs &a, cudaStream_t st, int *parts) {
-    constexpr int C16 = 16 / V;  // vectors of 16 columns
-    if (a.d <= 8 * V) return backward_cfg<T, V, 1, 8>(a, st, parts);
-    if (a.d <= 32 * V) return backward_cfg<T, V, 1, 32>(a, st, parts);
-    if (a.d <= 32 * 16) return backward_cfg<T, V, C16, 32>(a, st, parts);
-    if (a.d <= kThreads * V) return backward_cfg<T, V, 1, kThreads>(a, st, parts);
-    if (a.d <= kThreads * 16) return backward_cfg<T, V, C16, kThreads>(a, st, parts);
-    if (a.d <= kThreads * 32) return backward_cfg<T, V, 2 * C16, kThreads>(a, st, parts);
+// Up to 16 columns a thread (their sums and values take four registers each), and as few
+// threads a row as that allows.
+template <typename T>
+cudaError_t backward_vectors(const LayerNormArgs &a, cudaStream_t st, int *parts) {
+    constexpr int V = kVec<T>, C16 = 16 / V;
+    if (a.d <= 8 * V) return backward_ring<T, 1, 8>(a, st, parts);
+    if (a.d <= 32 * V) return backward_ring<T, 1, 32>(a, st, parts);
+    if (a.d <= 32 * 16) return backward_ring<T, C16, 32>(a, st, parts);
+    if (a.d <= 64 * 12 && C16 == 4) return backward_ring<T, 3, 64>(a, st, parts);
+    if (a.d <= 64 * 16) return backward_ring<T, C16, 64>(a, st, parts);
+    if (a.d <= 128 * 16) return backward_ring<T, C16, 128>(a, st, parts);
+    if (a.d <= 256 * 16) return backward_ring<T, C16, 256>(a, st, parts);
+    return backward_long<T>(a, st, parts);
+}
+
+template <typename T>
+cudaError_t backward_scalars(const LayerNormArgs &a, cudaStream_t st, int *parts) {
+    if (a.d <= 8) return backward_elements<T, 1, 8>(a, st, parts);
+    if (a.d <= 32) return backward_elements<T, 1, 32>(a, st, parts);
+    if (a.d <= 32 * 4) return backward_elements<T, 4, 32>(a, st, parts);
+    if (a.d <= 32 * 8) return backward_elements<T, 8, 32>(a, st, parts);
+    if (a.d <= 32 * 16) return backward_elements<T, 16, 32>(a, st, parts);
+    if (a.d <= 64 * 16) return backward_elements<T, 16, 64>(a, st, parts);
+    if (a.d <= 128 * 16) return backward_elements<T, 16, 128>(a, st, parts);
+    if (a.d <= 256 * 16) return backward_elements<T, 16, 256>(a, st, parts);
     return backward_long<T>(a, st, parts);
 }
 
@@ -449,12 +627,12 @@ cudaError_t backward_t(const LayerNormArgs &a, cudaStream_t st) {
     int parts = 0;
     cudaError_t e = cudaSuccess;
     if (a.N > 0 && (a.Y || a.dgamma || a.dbeta))
-        e = rows_in_vectors<T>(a) ? backward_v<T, kVec<T>>(a, st, &parts)
-                                  : backward_v<T, 1>(a, st, &parts);
+        e = rows_in_vectors<T>(a) ? backward_vectors<T>(a, st, &parts)
+                                  : backward_scalars<T>(a, st, &parts);
     if (e != cudaSuccess || (!a.dgamma && !a.dbeta)) return e;
     e = launch_pdl(layer_norm_join_kernel,
                    dim3(static_cast<unsigned>(ceil_div(2 * static_cast<int64_t>(a.d), 32))),
-                   dim3(kThreads), 0, st, static_cast<const float *>(a.part), parts,
+                   dim3(1024), 0, st, static_cast<const float *>(a.part), parts,
                    static_cast<int64_t>(a.d), a.dgamma, a.dbeta);
     if (e == cudaSuccess) note_launch();
     return e;

@@ -122,23 +122,25 @@ __global__ void __launch_bounds__(256) stage_kernel(const StageArgs a) {
     }
 }
 
-// db = the sum of the parts: 32 columns a block, 8 runs of parts side by side.
-__global__ void __launch_bounds__(256)
+// db = the sum of the parts: 32 columns a block, 32 runs of parts side by side.
+__global__ void __launch_bounds__(1024)
     col_join_kernel(const float *__restrict__ part, int parts, int cols, float *__restrict__ db) {
-    __shared__ float red[8][33];
+    __shared__ float red[32][33];
     pdl_wait();
     pdl_trigger();
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + x;
     float s = 0.f;
-    if (c < cols)
-        for (int p = y; p < parts; p += 8) s += part[static_cast<int64_t>(p) * cols + c];
+    if (c < cols) {
+#pragma unroll 8
+        for (int p = y; p < parts; p += 32) s += part[static_cast<int64_t>(p) * cols + c];
+    }
     red[y][x] = s;
     __syncthreads();
-    if (y == 0 && c < cols) {
-        for (int t = 1; t < 8; ++t) s += red[t][x];
-        db[c] = s;
-    }
+    // warp y sums the runs of column y
+    s = warp_sum_f(red[x][y]);
+    const int64_t o = static_cast<int64_t>(blockIdx.x) * 32 + y;
+    if (x == 0 && o < cols) db[o] = s;
 }
 
 int stage_tx(int cols) {
@@ -428,7 +430,7 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
         if ((e = launch_stage<T>(s, st)) != cudaSuccess) return e;
     }
     if (a.db) {
-        e = launch_pdl(col_join_kernel, dim3(static_cast<unsigned>(ceil_div(a.m, 32))), dim3(256),
+        e = launch_pdl(col_join_kernel, dim3(static_cast<unsigned>(ceil_div(a.m, 32))), dim3(1024),
                        0, st, ws_ptr<const float>(ws, L.col), stage_parts(a.N, a.m), a.m, a.db);
         if (e != cudaSuccess) return e;
         note_launch();

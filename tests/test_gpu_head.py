@@ -155,6 +155,24 @@ def test_layer_norm_backward(fk, N, d, dtype):
     assert torch.equal(dg2, dg) and torch.equal(db2, db)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,d", [(70, 768), (33, 4096), (40, 129), (9, 9000)])
+def test_layer_norm_backward_far_from_zero(fk, N, d, dtype):
+    """A mean a thousand times the spread: h = (x - mean) rstd must not be formed as a
+    difference of products."""
+    t = TYPES[dtype]
+    X, dY = rnd((N, d), t, 1, shift=1000.0), rnd((N, d), t, 5)
+    _, m, r = ref.layer_norm(X, None, None, 1e-5)
+    m, r = m.float(), r.float()
+    dX = torch.empty_like(X)
+    dg, db = torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    fk.fk_layer_norm_backward(dY, X, None, m, r, dX, dg, db,
+                              fk.layer_norm_backward_workspace(N, d, t))
+    want, tol = ref.layer_norm_backward(dY, X, None, m, r), lnb_tols(dY, X, None, m, r, t)
+    for name, a, b, c in zip(("dX", "dgamma", "dbeta"), (dX, dg, db), want, tol):
+        within(a, b, c, name)
+
+
 # ---------------------------------------------------------------------------------- linear
 
 def act_err(z, y, ez, slope_max=1.13):
