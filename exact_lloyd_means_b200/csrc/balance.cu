@@ -19,36 +19,55 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxStages = 8;         // slots of the ring of rows
-constexpr int kRingBytes = 64 << 10;  // its size: two or three blocks an SM
+constexpr int kRingBytes = 48 << 10;  // its size: three blocks an SM
 constexpr int kOneBlockLabels = 1 << 15;  // counted by one block in one launch
 constexpr int kSharedCells = 12288;       // counters kept in shared memory (48 KB)
 
-// Counts of one run of labels: in shared memory, then (several blocks) added to the zeroed
-// totals.  Integer atomics: the order does not change the sums.
+// Counts of one run of rows: in shared memory, then (several blocks) added to the zeroed
+// totals; or, with so many cells that a block meets most of them at most once or twice, in
+// the totals at once, equal labels of a warp together.  Integer atomics: the order does not
+// change the sums.
 template <bool ONE>
 __global__ void __launch_bounds__(1024)
-    balance_counts_kernel(const int32_t *__restrict__ labels, int64_t N, int top, int K,
+    balance_counts_kernel(const int32_t *__restrict__ labels, int64_t N, int top, int K, int local,
                           int32_t *__restrict__ counts, int32_t *__restrict__ rows) {
     extern __shared__ int32_t hist[];
     __shared__ int32_t srows;
     pdl_wait();
     pdl_trigger();
-    const bool local = K <= kSharedCells;
     if (local)
         for (int k = threadIdx.x; k < K; k += blockDim.x) hist[k] = 0;
     if (threadIdx.x == 0) srows = 0;
     __syncthreads();
-    int32_t *h = local ? hist : counts;
-    int mine = 0;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < N;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        bool any = false;
-        for (int t = 0; t < top; ++t) {
-            const int32_t l = labels[i * top + t];
-            if (l >= 0 && l < K) {
-                any = true;
-                atomicAdd(h + l, 1);
+    const int64_t i0 = N * blockIdx.x / gridDim.x, i1 = N * (blockIdx.x + 1) / gridDim.x;
+    // every selection, four loads ahead
+    const int64_t e = i1 * top, stride = blockDim.x;
+    for (int64_t j0 = i0 * top; j0 < e; j0 += 4 * stride) {
+        int32_t l[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t j = j0 + u * stride + threadIdx.x;
+            l[u] = j < e ? labels[j] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const bool in = l[u] >= 0 && l[u] < K;
+            if (local) {
+                if (in) atomicAdd(hist + l[u], 1);
+            } else {
+                const uint32_t same = __match_any_sync(0xffffffffu, in ? l[u] : -1);
+                if (in && (threadIdx.x & 31) == __ffs(same) - 1)
+                    atomicAdd(counts + l[u], __popc(same));
             }
+        }
+    }
+    // rows with any selection
+    int mine = 0;
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += stride) {
+        bool any = false;
+        for (int t = 0; t < top && !any; ++t) {
+            const int32_t l = labels[i * top + t];
+            any = l >= 0 && l < K;
         }
         mine += any;
     }
@@ -213,7 +232,7 @@ __device__ __forceinline__ float vec_max(const uint4 *u, int n, uint16_t) {
 // instruction where there is one, and an exponent is one multiply-add (scale2 s - scale2 m)
 // unless scale2 m would overflow.
 template <typename T, int NV, int TPR>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
     balance_ring_kernel(const T *S, T *dS, const LossArgs a, int stages,
                         uint32_t *__restrict__ err, uint64_t wait_ns) {
     constexpr int V = kVec<T>, H = V / 2, G = kThreads / TPR;
@@ -222,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     __shared__ uint64_t full[kMaxStages];
     __shared__ uint32_t abort_flag;
     extern __shared__ __align__(128) uint8_t space[];
-    float *f = reinterpret_cast<float *>(space);
-    uint8_t *ring = space + (a.K * 4 + 127) / 128 * 128;
+    float4 *f = reinterpret_cast<float4 *>(space);  // four columns of a thread; then TPR threads
+    uint8_t *ring = space + NV * TPR * V * 4;
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) ptx::mbar_init(&full[s], 1);
@@ -246,8 +265,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (threadIdx.x == 0)
         for (int s = 0; s < stages; ++s) bring(first + s * step, s);
     const LossScales c(a);
-    for (int k = threadIdx.x; k < a.K; k += kThreads)
-        f[k] = static_cast<float>(a.counts[k]) * c.unit;
+    for (int k = threadIdx.x; k < a.K; k += kThreads) {
+        const int v = k / V, q = (v / TPR * (H / 2) + k % V / 4) * TPR + v % TPR;
+        reinterpret_cast<float *>(f + q)[k % 4] = static_cast<float>(a.counts[k]) * c.unit;
+    }
     __syncthreads();
     const float scale2 = a.scale * 1.44269504f;
     const F2 scale22 = f2(scale2, scale2);
@@ -255,11 +276,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     int slot = 0, stage = 0;
     uint32_t phase = 0;
     int64_t i = first + grp;
-    bool keep = i < a.N && row_selects(a, i);
+    // the first selection of the next row, read a turn ahead (the others only if it is none)
+    int32_t next = i < a.N ? a.labels[i * a.top] : -1;
     T *out = dS + i * a.K + t * V;
     for (int64_t i0 = first; i0 < a.N; i0 += step, i += step, out += step * a.K) {
-        const bool on = keep;
-        keep = i + step < a.N && row_selects(a, i + step);
+        const int32_t lab = next;
+        if (i + step < a.N) next = a.labels[(i + step) * a.top];
+        const bool on = i < a.N && ((lab >= 0 && lab < a.K) || (a.top > 1 && row_selects(a, i)));
         // a wait that runs out is recorded, and the pass runs to its end without its data
         if (!ptx::mbar_wait(&full[stage], phase, &abort_flag, wait_ns)) {
             *const_cast<volatile uint32_t *>(&abort_flag) = 1u;
@@ -282,26 +305,32 @@ __global__ void __launch_bounds__(kThreads, 2)
         F2 e[NV][H];
         F2 z2 = f2(0.f, 0.f), t2 = z2;
 #pragma unroll
+        for (int n = 0; n < NV; ++n) unpack2(u[n], e[n]);
+        if (direct) {
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+#pragma unroll
+                for (int k = 0; k < H; ++k) e[n][k] = fma2(e[n][k], scale22, off);
+        } else {  // (also where base is NaN)
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+#pragma unroll
+                for (int k = 0; k < H; ++k)
+                    e[n][k] = mul2(scale22, add2(e[n][k], f2(-base, -base)));
+        }
+#pragma unroll
         for (int n = 0; n < NV; ++n) {
-            unpack2(u[n], e[n]);
-            const float4 *fp = reinterpret_cast<const float4 *>(f + (n * TPR + t) * V);
 #pragma unroll
             for (int k = 0; k < H; ++k) {
                 float lo, hi;
-                if (direct) {
-                    split(fma2(e[n][k], scale22, off), lo, hi);
-                } else {  // (also where base is NaN)
-                    split(e[n][k], lo, hi);
-                    lo = scale2 * (lo - base);
-                    hi = scale2 * (hi - base);
-                }
+                split(e[n][k], lo, hi);
                 e[n][k] = f2(exp2_fast(lo), exp2_fast(hi));
                 z2 = add2(z2, e[n][k]);
             }
             if ((n * TPR + t) * V < a.K) {
 #pragma unroll
                 for (int k = 0; k < H; k += 2) {
-                    const float4 q = fp[k / 2];
+                    const float4 q = f[(n * (H / 2) + k / 2) * TPR + t];
                     t2 = fma2(e[n][k], f2(q.x, q.y), t2);
                     t2 = fma2(e[n][k + 1], f2(q.z, q.w), t2);
                 }
@@ -327,11 +356,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             if ((n * TPR + t) * V < a.K) {
-                const float4 *fp = reinterpret_cast<const float4 *>(f + (n * TPR + t) * V);
                 F2 v[H];
 #pragma unroll
                 for (int k = 0; k < H; k += 2) {
-                    const float4 q = fp[k / 2];
+                    const float4 q = f[(n * (H / 2) + k / 2) * TPR + t];
                     v[k] = mul2(e[n][k], fma2(f2(q.x, q.y), gp2, gt2));
                     v[k + 1] = mul2(e[n][k + 1], fma2(f2(q.z, q.w), gp2, gt2));
                 }
@@ -495,7 +523,7 @@ cudaError_t loss_ring(const BalanceArgs &b, const LossArgs &a, int *grid, cudaSt
     if (e != cudaSuccess) return e;
     *grid = loss_grid(b, kThreads / TPR);
     return launch_pdl(kernel, dim3(*grid), dim3(kThreads),
-                      round_up(a.K * 4, 128) + static_cast<size_t>(stages) * slot, st,
+                      NV * TPR * kVec<T> * 4 + static_cast<size_t>(stages) * slot, st,
                       static_cast<const T *>(b.S), static_cast<T *>(b.dS), a, stages, b.err,
                       kDefaultWaitNs);
 }
@@ -551,12 +579,10 @@ int64_t balance_parts(int64_t N, int K) {
 
 cudaError_t launch_balance_counts(const int32_t *labels, int64_t N, int top, int K,
                                   int32_t *counts, int32_t *rows, cudaStream_t st) {
-    const bool local = K <= kSharedCells;
-    const size_t smem = local ? sizeof(int32_t) * K : 0;
     cudaError_t e;
-    if (local && N * top <= kOneBlockLabels) {
-        e = launch_pdl(balance_counts_kernel<true>, dim3(1), dim3(1024), smem, st, labels, N, top,
-                       K, counts, rows);
+    if (K <= kSharedCells && N * top <= kOneBlockLabels) {
+        e = launch_pdl(balance_counts_kernel<true>, dim3(1), dim3(1024), sizeof(int32_t) * K, st,
+                       labels, N, top, K, 1, counts, rows);
         if (e == cudaSuccess) note_launch();
         return e;
     }
@@ -566,9 +592,11 @@ cudaError_t launch_balance_counts(const int32_t *labels, int64_t N, int top, int
     if (e != cudaSuccess) return e;
     note_launch();
     if (N == 0) return e;
-    const int64_t g = ceil_div(N, 1024);
-    e = launch_pdl(balance_counts_kernel<false>, dim3(static_cast<unsigned>(g < 148 ? g : 148)),
-                   dim3(1024), smem, st, labels, N, top, K, counts, rows);
+    int64_t g = ceil_div(N * top, 1024);
+    if (g > 148) g = 148;
+    const int local = K <= kSharedCells && N * top / g >= 2 * static_cast<int64_t>(K);
+    e = launch_pdl(balance_counts_kernel<false>, dim3(static_cast<unsigned>(g)), dim3(1024),
+                   local ? sizeof(int32_t) * K : 0, st, labels, N, top, K, local, counts, rows);
     if (e == cudaSuccess) note_launch();
     return e;
 }

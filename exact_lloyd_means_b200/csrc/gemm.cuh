@@ -15,10 +15,13 @@ struct GemmOperand {
     bool mn_major;
 };
 
-// How a product is cut: tiles of 128 * cg rows by bn columns (cg CTAs each), the depth in
-// `splits` parts whose partial products are joined afterwards.
+// How a product is cut: tiles of 128 * cg rows by bn columns (cg CTAs each).  The first `full`
+// tiles take the whole depth; that of the others, which would leave most of the GPU idle, is
+// cut into `splits` parts, whose partial products are joined afterwards.
 struct GemmPlan {
     int cg, bn, splits;
+    int64_t full, tail;
+    int64_t tile() const { return int64_t(128) * cg * bn; }
 };
 
 struct GemmArgs {
@@ -31,30 +34,40 @@ struct GemmArgs {
     int act;
     const void *R;
     void *C, *Z;
-    float *part;  // [splits][rows][round_up(cols, 8)] when splits > 1
+    float *part;  // [tail tile][split][row][column] of whole tiles, when splits > 1
     uint32_t *err;
 };
 
 GemmPlan gemm_plan(int64_t rows, int64_t cols, int64_t depth, int planes);
-inline size_t gemm_part_bytes(int64_t rows, int64_t cols, const GemmPlan &p) {
-    return p.splits > 1 ? sizeof(float) * p.splits * rows * round_up(cols, 8) : 0;
+inline size_t gemm_part_bytes(const GemmPlan &p) {
+    return p.splits > 1 ? sizeof(float) * p.tail * p.splits * p.tile() : 0;
 }
 cudaError_t launch_gemm(const GemmArgs &a, const GemmPlan &p, cudaStream_t st);
 
 // ----------------------------------------------------------------- epilogue
+// One branch for all the values, which keeps their chains of dependent instructions side by
+// side.
 template <int P, int V>
 __device__ __forceinline__ void act_values(float (&z)[P][V], int act) {
+    static_assert(P * V % 2 == 0 || P * V == 1, "pairs");
+    auto all = [&](int which) {
+        if constexpr (P * V == 1) {
+            z[0][0] = act_value(z[0][0], which);
+        } else {
+#pragma unroll
+            for (int i = 0; i < P * V; i += 2) {
+                float &lo = z[i / V][i % V], &hi = z[(i + 1) / V][(i + 1) % V];
+                split(act_value2(f2(lo, hi), which), lo, hi);
+            }
+        }
+    };
     if (act == FK_ACT_NONE) return;
-    if (act == FK_ACT_RELU) {
-#pragma unroll
-        for (int i = 0; i < P * V; ++i) z[i / V][i % V] = act_value(z[i / V][i % V], FK_ACT_RELU);
-    } else if (act == FK_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < P * V; ++i) z[i / V][i % V] = act_value(z[i / V][i % V], FK_ACT_GELU);
-    } else {
-#pragma unroll
-        for (int i = 0; i < P * V; ++i) z[i / V][i % V] = act_value(z[i / V][i % V], FK_ACT_SILU);
-    }
+    if (act == FK_ACT_RELU)
+        all(FK_ACT_RELU);
+    else if (act == FK_ACT_GELU)
+        all(FK_ACT_GELU);
+    else
+        all(FK_ACT_SILU);
 }
 
 struct Epilogue {
@@ -76,8 +89,7 @@ struct Pieces {
 // z: their products without the bias.  Each output is rounded once from fp32.  The residual
 // is read before anything of the pieces is written (C may be R).  The additions
 // are kept apart from the activation's products, so that the bits do not depend on which
-// outputs are asked for; the activation is one branch for all pieces, which keeps their
-// chains of dependent instructions side by side.
+// outputs are asked for.
 template <typename T, int V, bool ALL, int P>
 __device__ __forceinline__ void epilogue_pieces(const Epilogue &e, const Pieces &o, int bvec,
                                                 float (&z)[P][V]) {

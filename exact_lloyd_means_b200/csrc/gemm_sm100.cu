@@ -62,7 +62,7 @@ struct GemmShape {
     int terms;    // products per chunk: 1, or 6 of three planes
     int a_mn, b_mn;
     int64_t tiles_r, tiles_c, units;
-    int64_t part_ld;
+    int64_t full, tail;  // tiles with the whole depth, tiles with their depth cut
 };
 
 // The plane of A and of B in product t of the six.
@@ -73,26 +73,40 @@ __device__ __forceinline__ int term_b(int terms, int t) {
     return terms == 1 ? 0 : (0x001012 >> (4 * t)) & 3;  // 2 1 0 1 0 0
 }
 
-// Unit u: its tile (bands of kBandRows row tiles, rows fastest within a band, so that the
-// tiles running side by side share their operands in L2) and its chunks of the depth.
-struct Unit {
-    int64_t tr, tc;
-    int split, k0, k1;
-};
-template <int CG>
-__device__ __forceinline__ Unit unit_of(const GemmShape &s, int64_t u) {
-    Unit r;
-    const int64_t tiles = s.tiles_r * s.tiles_c;
-    r.split = static_cast<int>(u / tiles);
-    const int64_t t = u - r.split * tiles;
+// Tile t in the order of work: bands of kBandRows row tiles, rows fastest within a band, so that
+// the tiles running side by side share their operands in L2.
+__host__ __device__ __forceinline__ void tile_of(const GemmShape &s, int64_t t, int64_t &tr,
+                                                 int64_t &tc) {
     const int64_t per_band = kBandRows * s.tiles_c;
     const int64_t band = t / per_band, in = t - band * per_band;
     const int64_t left = s.tiles_r - band * kBandRows;
     const int64_t h = left < kBandRows ? left : kBandRows;
-    r.tc = in / h;
-    r.tr = band * kBandRows + (in - r.tc * h);
-    r.k0 = static_cast<int>(static_cast<int64_t>(s.nkc) * r.split / s.splits);
-    r.k1 = static_cast<int>(static_cast<int64_t>(s.nkc) * (r.split + 1) / s.splits);
+    tc = in / h;
+    tr = band * kBandRows + (in - tc * h);
+}
+
+// Unit u: its tile, its chunks of the depth and, where they are not all, its partial product.
+struct Unit {
+    int64_t tr, tc, part;
+    int k0, k1;
+};
+__device__ __forceinline__ Unit unit_of(const GemmShape &s, int64_t u) {
+    Unit r;
+    int64_t t = u;
+    r.part = -1;
+    r.k0 = 0;
+    r.k1 = s.nkc;
+    if (u >= s.full) {
+        const int64_t v = u - s.full;
+        const int split = static_cast<int>(v / s.tail);
+        t = s.full + (v - split * s.tail);
+        if (s.splits > 1) {
+            r.part = (v - split * s.tail) * s.splits + split;
+            r.k0 = static_cast<int>(static_cast<int64_t>(s.nkc) * split / s.splits);
+            r.k1 = static_cast<int>(static_cast<int64_t>(s.nkc) * (split + 1) / s.splits);
+        }
+    }
+    tile_of(s, t, r.tr, r.tc);
     return r;
 }
 
@@ -166,7 +180,7 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, OV>::kThreads, 1)
             uint32_t stage = 0, phase = 0;
             bool ok = true;
             for (int64_t u = first; u < sh.units && ok; u += step) {
-                const Unit un = unit_of<CG>(sh, u);
+                const Unit un = unit_of(sh, u);
                 const int r0 = static_cast<int>(un.tr * (kBM * CG) + rank * kBM);
                 const int c0 = static_cast<int>(un.tc * BN + rank * Cfg::kBRows);
                 for (int t = 0; t < sh.terms && ok; ++t) {
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, OV>::kThreads, 1)
             uint32_t stage = 0, phase = 0, it = 0;
             bool ok = true;
             for (int64_t u = first; u < sh.units && ok; u += step, ++it) {
-                const Unit un = unit_of<CG>(sh, u);
+                const Unit un = unit_of(sh, u);
                 const uint32_t acc = it & 1u;
                 if (!ptx::mbar_wait(&tempty[acc], ((it >> 1) & 1u) ^ 1u, abort_flag, wait_ns)) {
                     gemm_timeout(abort_flag, err);
@@ -285,7 +299,7 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, OV>::kThreads, 1)
             CG == 2 ? ptx::mapa_shared(ptx::smem_u32(tempty), 0) : 0u;
         uint32_t it = 0;
         for (int64_t u = first; u < sh.units; u += step, ++it) {
-            const Unit un = unit_of<CG>(sh, u);
+            const Unit un = unit_of(sh, u);
             const uint32_t acc = it & 1u;
             const int64_t r0 = un.tr * (kBM * CG) + rank * kBM + q * 32;
             const int64_t c0 = un.tc * BN + g * Cfg::kGroupCols;
@@ -314,17 +328,14 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, OV>::kThreads, 1)
                             ptx::mbar_arrive(&tempty[acc]);
                     }
                 }
-                if (sh.splits > 1) {  // fp32 partial products, rows of a multiple of 8
-                    if (r0 + lane < sh.rows) {
-                        float *dst = part + (un.split * sh.rows + r0 + lane) * sh.part_ld + col;
+                if (un.part >= 0) {  // fp32 partial products, the whole tile
+                    float *dst = part + (un.part * CG + rank) * (kBM * BN) +
+                                 (q * 32 + lane) * BN + g * Cfg::kGroupCols + c * 32;
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            if (col + j < sh.part_ld) {
-                                const float o[8] = {v[j],     v[j + 1], v[j + 2], v[j + 3],
-                                                    v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
-                                Raw<float, 8>::put(dst + j, o);
-                            }
-                        }
+                    for (int j = 0; j < 32; j += 8) {
+                        const float o[8] = {v[j],     v[j + 1], v[j + 2], v[j + 3],
+                                            v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
+                        Raw<float, 8>::put(dst + j, o);
                     }
                 } else if constexpr (OV > 1) {
                     float z[32 / OV][OV];
@@ -381,26 +392,32 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, OV>::kThreads, 1)
     }
 }
 
-// Join the partial products of a split depth, in order, and apply the epilogue.
+// Join the partial products of the tail tiles, in order, and apply the epilogue.  Block (x,
+// y): rows of tail tile y.
 template <typename T, int V>
 __global__ void __launch_bounds__(256)
-    gemm_join_kernel(const float *__restrict__ part, int splits, int64_t rows, int64_t part_ld,
-                     int64_t per_row, const Epilogue ep, int bvec) {
+    gemm_join_kernel(const float *__restrict__ part, const GemmShape s, int tile_rows, int bn,
+                     const Epilogue ep, int bvec) {
     pdl_wait();
     pdl_trigger();
-    const int64_t total = rows * per_row;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < total;
-         t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t row = t / per_row, col = (t - row * per_row) * V;
-        const Pieces o{row * ep.cols + col, 0, col, 0, 1u};
+    int64_t tr, tc;
+    tile_of(s, s.full + blockIdx.y, tr, tc);
+    const int64_t size = static_cast<int64_t>(tile_rows) * bn;
+    const float *base = part + blockIdx.y * s.splits * size;
+    const int per_row = bn / V;
+    for (int t = blockIdx.x * 256 + threadIdx.x; t < tile_rows * per_row; t += gridDim.x * 256) {
+        const int lr = t / per_row, lc = (t - lr * per_row) * V;
+        const int64_t row = tr * tile_rows + lr, col = tc * bn + lc;
+        if (row >= s.rows || col >= s.cols) continue;
+        const Pieces o{row * s.cols + col, 0, col, 0, 1u};
         float z[1][V];
 #pragma unroll
         for (int j = 0; j < V; ++j) z[0][j] = 0.f;
-        const float *p = part + row * part_ld + col;
+        const float *p = base + lr * bn + lc;
 #pragma unroll 4
-        for (int s = 0; s < splits; ++s) {
+        for (int i = 0; i < s.splits; ++i) {
             float f[V];
-            load_params<V>(p + s * rows * part_ld, 1, f);
+            load_params<V>(p + i * size, 1, f);
 #pragma unroll
             for (int j = 0; j < V; ++j) z[0][j] += f[j];
         }
@@ -449,8 +466,9 @@ cudaError_t launch_cfg(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
     s.b_mn = a.B.mn_major;
     s.tiles_r = ceil_div(a.rows, kBM * CG);
     s.tiles_c = ceil_div(a.cols, BN);
-    s.units = s.tiles_r * s.tiles_c * p.splits;
-    s.part_ld = round_up(a.cols, 8);
+    s.full = p.full;
+    s.tail = p.tail;
+    s.units = p.full + p.tail * p.splits;
     const int bvec = aligned(a.bias, 16);
     Epilogue ep{};
     ep.bias = a.bias;
@@ -479,12 +497,13 @@ cudaError_t launch_cfg(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
     note_launch();
     if (p.splits > 1) {
         constexpr int JV = OV > kVec<T> ? kVec<T> : OV;  // 16 bytes of output a thread
-        const int64_t per_row = ceil_div(a.cols, JV);
-        const int64_t g = ceil_div(a.rows * per_row, 256),
-                      cap = static_cast<int64_t>(device_sm_count()) * 8;
-        e = launch_pdl(gemm_join_kernel<T, JV>, dim3(static_cast<unsigned>(g < cap ? g : cap)),
-                       dim3(256), 0, st, static_cast<const float *>(a.part), p.splits, a.rows,
-                       s.part_ld, per_row, ep, bvec);
+        const int64_t want = ceil_div(static_cast<int64_t>(device_sm_count()) * 8, p.tail);
+        const int64_t most = p.tile() / JV / 256;
+        e = launch_pdl(gemm_join_kernel<T, JV>,
+                       dim3(static_cast<unsigned>(want < most ? want : most),
+                            static_cast<unsigned>(p.tail)),
+                       dim3(256), 0, st, static_cast<const float *>(a.part), s, kBM * CG, BN, ep,
+                       bvec);
         if (e == cudaSuccess) note_launch();
     }
     return e;
@@ -513,31 +532,34 @@ cudaError_t launch_t(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
 
 // The cheapest cut by a model in SM cycles: a chunk of 64 of the depth takes the time its
 // operands take to arrive (64 bytes a cycle and SM) or its products, whichever is longer: 512
-// for the pair's 256 x 256 tile, 512 for 128 x 128, 384 for 128 x 64; a unit fills its ring
-// and empties its last accumulator once (about 4000); joining a split depth costs a launch
-// (about 4000) and its traffic (about 3000 bytes a cycle through L2).  A part of the depth
-// keeps at least four chunks.
+// for the pair's 256 x 256 tile, 512 for 128 x 128, 384 for 128 x 64; the ring fills and the
+// last accumulator empties once (about 4000).  Tiles run in waves of as many as the GPU
+// holds; those of the last, partial wave may have their depth cut so that it is spread over
+// the GPU, in parts of at least four chunks: that costs a launch (about 4000) and the partial
+// products' way through L2 (about 3000 bytes a cycle).
 GemmPlan gemm_plan(int64_t rows, int64_t cols, int64_t depth, int planes) {
     const int64_t nkc = ceil_div(depth, kBK);
     const int terms = planes == 3 ? 6 : 1;
     static constexpr struct {
         int cg, bn, cycles;
     } kCfg[3] = {{2, 256, 512}, {1, 128, 512}, {1, 64, 384}};
-    GemmPlan best{1, 64, 1};
+    GemmPlan best{};
     double best_cost = -1;
     for (const auto &c : kCfg) {
         const int64_t tiles = ceil_div(rows, kBM * c.cg) * ceil_div(cols, c.bn);
         const int64_t slots = 148 / c.cg;
-        for (int s = 1; s <= 32; ++s) {
-            if (s > 1 && nkc / s < 4) break;
-            const double waves = static_cast<double>(ceil_div(tiles * s, slots));
-            double cost = waves * (static_cast<double>(ceil_div(nkc, s)) * terms * c.cycles) +
-                          4000 + 500 * waves;
-            if (s > 1)
-                cost += 4000 + 8.0 * s * static_cast<double>(rows) * round_up(cols, 8) / 3000;
+        GemmPlan p{c.cg, c.bn, 1, tiles / slots * slots, tiles % slots};
+        for (p.splits = 1; p.splits <= 32; ++p.splits) {
+            if (p.splits > 1 && (p.tail == 0 || nkc / p.splits < 4)) break;
+            const double waves = static_cast<double>(p.full / slots);
+            const double last = static_cast<double>(ceil_div(p.tail * p.splits, slots));
+            double cost = 4000 + (waves + last) * 500 +
+                          (waves * nkc + last * ceil_div(nkc, p.splits)) * terms * c.cycles;
+            if (p.splits > 1)
+                cost += 4000 + 8.0 * static_cast<double>(p.tail * p.splits * p.tile()) / 3000;
             if (best_cost < 0 || cost < best_cost) {
                 best_cost = cost;
-                best = GemmPlan{c.cg, c.bn, s};
+                best = p;
             }
         }
     }

@@ -281,43 +281,76 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // Stegun 7.1.26: erf within 1.5e-7, so Phi within 0.75e-7 (1.3 units of 2^-24), in two special
 // function calls and about ten products; with CUDA's erff, several times the instructions,
 // the epilogue of a 768-deep product is bound by its arithmetic.
-__device__ __forceinline__ float half_erfc(float z, float *e) {
-    const float t = rcp_fast(1.f + 0.23164190f * fabsf(z));  // 0.3275911 / sqrt(2)
-    float p = 0.5f * 1.061405429f;
-    p = p * t - 0.5f * 1.453152027f;
-    p = p * t + 0.5f * 1.421413741f;
-    p = p * t - 0.5f * 0.284496736f;
-    p = p * t + 0.5f * 0.254829592f;
-    *e = exp2_fast(-0.72134752f * z * z);
-    return p * t * *e;
+__device__ __forceinline__ F2 half_erfc2(F2 z, F2 a, F2 *e) {
+    float lo, hi;
+    split(fma2(a, f2(0.23164190f, 0.23164190f), f2(1.f, 1.f)), lo, hi);  // 0.3275911 / sqrt(2)
+    const F2 t = f2(rcp_fast(lo), rcp_fast(hi));
+    const auto twice = [](float c) { return f2(c, c); };
+    F2 p = fma2(twice(0.5f * 1.061405429f), t, twice(-0.5f * 1.453152027f));
+    p = fma2(p, t, twice(0.5f * 1.421413741f));
+    p = fma2(p, t, twice(-0.5f * 0.284496736f));
+    p = fma2(p, t, twice(0.5f * 0.254829592f));
+    split(mul2(mul2(z, z), twice(-0.72134752f)), lo, hi);
+    *e = f2(exp2_fast(lo), exp2_fast(hi));
+    return mul2(mul2(p, t), *e);
 }
 
-// act(z): relu max(z, 0); GELU z Phi(z) with the normal distribution function Phi (the
-// erf form); SiLU z / (1 + exp(-z)).  NaN stays NaN; at infinity, the
-// limits of GELU, and for SiLU what its formula gives.
-__device__ __forceinline__ float act_value(float z, int act) {
-    if (act == FK_ACT_RELU) return z > 0.f ? z : (z == z ? 0.f : z);
-    if (act == FK_ACT_GELU) {
-        float e;
-        const float h = half_erfc(z, &e);
-        return fmaxf(z, 0.f) - fminf(fabsf(z), 32.f) * h;  // (h = 0 long before 32; NaN stays)
-    }
-    if (act == FK_ACT_SILU) return z * rcp_fast(1.f + exp2_fast(-1.44269504f * z));
-    return z;
+__device__ __forceinline__ F2 abs2(F2 z) {
+    F2 r;
+    r.v = z.v & 0x7fffffff7fffffffull;
+    return r;
 }
-// act'(z); the slope of relu at 0 is 0.
-__device__ __forceinline__ float act_slope(float z, int act) {
-    if (act == FK_ACT_RELU) return z > 0.f ? 1.f : (z == z ? 0.f : z);
+
+// act(z) of a pair: relu max(z, 0); GELU z Phi(z) with the normal distribution function Phi
+// (the erf form), as max(z, 0) - |z| h (h is 0 long before |z| = 32); SiLU z / (1 + exp(-z)).
+// NaN stays NaN; at infinity, the limits of GELU, and for SiLU what its formula gives.
+__device__ __forceinline__ F2 act_value2(F2 z, int act) {
+    float lo, hi;
+    if (act == FK_ACT_RELU) {
+        split(z, lo, hi);
+        return f2(lo > 0.f ? lo : (lo == lo ? 0.f : lo), hi > 0.f ? hi : (hi == hi ? 0.f : hi));
+    }
     if (act == FK_ACT_GELU) {
-        float e;
-        const float h = half_erfc(z, &e);
-        return (z > 0.f ? 1.f - h : h) + z * 0.39894228f * e;
+        F2 e;
+        const F2 a = abs2(z), h = half_erfc2(z, a, &e);
+        float al, ah;
+        split(z, lo, hi);
+        split(a, al, ah);
+        return fma2(f2(-fminf(al, 32.f), -fminf(ah, 32.f)), h, f2(fmaxf(lo, 0.f), fmaxf(hi, 0.f)));
     }
     if (act == FK_ACT_SILU) {
-        const float s = rcp_fast(1.f + exp2_fast(-1.44269504f * z));
-        return s * (1.f + z * (1.f - s));
+        split(mul2(z, f2(-1.44269504f, -1.44269504f)), lo, hi);
+        split(add2(f2(exp2_fast(lo), exp2_fast(hi)), f2(1.f, 1.f)), lo, hi);
+        return mul2(z, f2(rcp_fast(lo), rcp_fast(hi)));
     }
-    return 1.f;
+    return z;
+}
+// act'(z) of a pair; the slope of relu at 0 is 0.
+__device__ __forceinline__ F2 act_slope2(F2 z, int act) {
+    float lo, hi;
+    if (act == FK_ACT_RELU) {
+        split(z, lo, hi);
+        return f2(lo > 0.f ? 1.f : (lo == lo ? 0.f : lo), hi > 0.f ? 1.f : (hi == hi ? 0.f : hi));
+    }
+    if (act == FK_ACT_GELU) {  // Phi + z phi, Phi = 1/2 + sign(z) (1/2 - h)
+        F2 e;
+        const F2 h = half_erfc2(z, abs2(z), &e);
+        F2 u = fma2(h, f2(-1.f, -1.f), f2(0.5f, 0.5f));
+        u.v ^= z.v & 0x8000000080000000ull;
+        return fma2(mul2(z, f2(0.39894228f, 0.39894228f)), e, add2(u, f2(0.5f, 0.5f)));
+    }
+    if (act == FK_ACT_SILU) {  // s + z s (1 - s)
+        split(mul2(z, f2(-1.44269504f, -1.44269504f)), lo, hi);
+        split(add2(f2(exp2_fast(lo), exp2_fast(hi)), f2(1.f, 1.f)), lo, hi);
+        const F2 s = f2(rcp_fast(lo), rcp_fast(hi));
+        return fma2(mul2(z, s), fma2(s, f2(-1.f, -1.f), f2(1.f, 1.f)), s);
+    }
+    return f2(1.f, 1.f);
+}
+__device__ __forceinline__ float act_value(float z, int act) {
+    float lo, hi;
+    split(act_value2(f2(z, z), act), lo, hi);
+    return lo;
 }
 
 }  // namespace fk

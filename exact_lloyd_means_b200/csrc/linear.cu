@@ -35,7 +35,7 @@ __device__ __forceinline__ void pieces(float x, uint16_t (&p)[3]) {
     p[2] = bf16_bits(r - bf16_val(p[1]));
 }
 
-struct StageArgs {
+struct StageJob {
     const void *src, *Z;  // rows x cols; Z non-null: multiply by act'(Z)
     int64_t rows;
     int cols;
@@ -44,81 +44,144 @@ struct StageArgs {
     uint16_t *out;   // planes [P][rows][ld], or null for column sums alone
     int64_t ld;
     float *colpart;  // [parts][cols], or null
-    int tx;          // threads across a row (a power of two up to 32), 8 columns each
+    int tx;          // threads across a row (a power of two), 8 columns each
+    int gx, parts;   // blocks across the columns, runs of rows
+};
+constexpr int kMaxJobs = 3;  // operands staged in one launch
+struct StageJobs {
+    StageJob job[kMaxJobs];
+    int first[kMaxJobs + 1];  // their first blocks
+    int n;
 };
 
-// Block (x, y): 8 * tx columns, the y-th of gridDim.y runs of rows.
+// Eight consecutive values as they lie in memory (zero where there is no column).
 template <typename T>
-__global__ void __launch_bounds__(256) stage_kernel(const StageArgs a) {
-    constexpr int P = sizeof(T) == 4 ? 3 : 1;
-    __shared__ float red[256][9];
-    pdl_wait();
-    pdl_trigger();
-    const int tx = threadIdx.x & (a.tx - 1), ty = threadIdx.x / a.tx, nty = 256 / a.tx;
-    const int64_t col = (static_cast<int64_t>(blockIdx.x) * a.tx + tx) * 8;
-    const int64_t i0 = a.rows * blockIdx.y / gridDim.y,
-                  i1 = a.rows * (blockIdx.y + 1) / gridDim.y;
-    const T *src = static_cast<const T *>(a.src), *Z = static_cast<const T *>(a.Z);
-    float sum[8] = {};
-    if (col < a.cols) {
-#pragma unroll 2
-        for (int64_t i = i0 + ty; i < i1; i += nty) {
-            float v[8], z[8];
-            auto load8 = [&](const T *p, float (&o)[8]) {
-                p += i * a.cols + col;
-                if (a.vec) {
+struct Eight {
+    uint4 u[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p, int64_t left, int vec) {
+        if (vec) {
 #pragma unroll
-                    for (int h = 0; h < 8 / kVec<T>; ++h) {
-                        float t[kVec<T>];
-                        unpack16(*reinterpret_cast<const uint4 *>(p + h * kVec<T>), t);
+            for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h)
+                u[h] = *reinterpret_cast<const uint4 *>(p + h * kVec<T>);
+        } else {
+            T *t = reinterpret_cast<T *>(u);
 #pragma unroll
-                        for (int j = 0; j < kVec<T>; ++j) o[h * kVec<T> + j] = t[j];
-                    }
-                } else {
+            for (int j = 0; j < 8; ++j) t[j] = j < left ? p[j] : T(0);
+        }
+    }
+    __device__ __forceinline__ void pairs(F2 (&o)[4]) const {
+        if constexpr (sizeof(T) == 2) {
+            unpack2(u[0], o);
+        } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = col + j < a.cols ? head_load(p + j) : 0.f;
-                }
-            };
-            load8(src, v);
-            if (Z != nullptr) {
-                load8(Z, z);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] *= act_slope(z[j], a.act);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += v[j];
-            if (a.out != nullptr) {
-                uint16_t *o = a.out + i * a.ld + col;
-                uint16_t pc[8][3];
-                if constexpr (P == 3) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) pieces(v[j], pc[j]);
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) {
-                        uint4 u;
-                        u.x = pc[0][p] | static_cast<uint32_t>(pc[1][p]) << 16;
-                        u.y = pc[2][p] | static_cast<uint32_t>(pc[3][p]) << 16;
-                        u.z = pc[4][p] | static_cast<uint32_t>(pc[5][p]) << 16;
-                        u.w = pc[6][p] | static_cast<uint32_t>(pc[7][p]) << 16;
-                        *reinterpret_cast<uint4 *>(o + p * a.rows * a.ld) = u;
-                    }
-                } else {  // a bf16 operand: G is rounded once
-                    *reinterpret_cast<uint4 *>(o) = pack16(v);
-                }
+            for (int h = 0; h < 2; ++h) {
+                F2 t[2];
+                unpack2(u[h], t);
+                o[2 * h] = t[0];
+                o[2 * h + 1] = t[1];
             }
         }
     }
+};
+
+template <typename T>
+__device__ __forceinline__ void stage_store(const StageJob &a, int64_t i, int64_t col,
+                                            const F2 (&v)[4]) {
+    uint16_t *o = a.out + i * a.ld + col;
+    if constexpr (sizeof(T) == 2) {  // a bf16 operand: G is rounded once
+        *reinterpret_cast<uint4 *>(o) = pack2(v);
+    } else {
+        uint16_t pc[8][3];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float lo, hi;
+            split(v[j], lo, hi);
+            pieces(lo, pc[2 * j]);
+            pieces(hi, pc[2 * j + 1]);
+        }
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            uint4 u;
+            u.x = pc[0][p] | static_cast<uint32_t>(pc[1][p]) << 16;
+            u.y = pc[2][p] | static_cast<uint32_t>(pc[3][p]) << 16;
+            u.z = pc[4][p] | static_cast<uint32_t>(pc[5][p]) << 16;
+            u.w = pc[6][p] | static_cast<uint32_t>(pc[7][p]) << 16;
+            *reinterpret_cast<uint4 *>(o + p * a.rows * a.ld) = u;
+        }
+    }
+}
+
+// A block of a job: 8 * tx columns, one of the job's runs of rows.
+template <typename T, int ACT>
+__device__ __forceinline__ void stage_rows(const StageJob &a, int64_t i0, int64_t i1, int64_t col,
+                                           int ty, int nty, F2 (&sum)[4]) {
+    const T *src = static_cast<const T *>(a.src) + col, *Z = static_cast<const T *>(a.Z) + col;
+    const int64_t left = a.cols - col;
+    constexpr int B = sizeof(T) == 2 ? 4 : 2;  // rows read before any is worked on
+    for (int64_t i = i0 + ty; i < i1; i += B * nty) {
+        Eight<T> x[B], y[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (i + b * nty < i1) {
+                x[b].load(src + (i + b * nty) * a.cols, left, a.vec);
+                if constexpr (ACT != FK_ACT_NONE)
+                    y[b].load(Z + (i + b * nty) * a.cols, left, a.vec);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (i + b * nty >= i1) break;
+            F2 v[4];
+            x[b].pairs(v);
+            if constexpr (ACT != FK_ACT_NONE) {
+                F2 z[4];
+                y[b].pairs(z);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], act_slope2(z[j], ACT));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[j] = add2(sum[j], v[j]);
+            if (a.out != nullptr) stage_store<T>(a, i + b * nty, col, v);
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) stage_kernel(const __grid_constant__ StageJobs jobs) {
+    __shared__ float red[256][9];
+    pdl_wait();
+    pdl_trigger();
+    int which = 0;
+    while (which + 1 < jobs.n && static_cast<int>(blockIdx.x) >= jobs.first[which + 1]) ++which;
+    const StageJob &a = jobs.job[which];
+    const int block = blockIdx.x - jobs.first[which];
+    const int by = block / a.gx, bx = block - by * a.gx;
+    const int tx = threadIdx.x & (a.tx - 1), ty = threadIdx.x / a.tx, nty = 256 / a.tx;
+    const int64_t col = (static_cast<int64_t>(bx) * a.tx + tx) * 8;
+    const int64_t i0 = a.rows * by / a.parts, i1 = a.rows * (by + 1) / a.parts;
+    F2 sum[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+    if (col < a.cols) {
+        const int act = a.Z != nullptr ? a.act : FK_ACT_NONE;
+        if (act == FK_ACT_NONE)
+            stage_rows<T, FK_ACT_NONE>(a, i0, i1, col, ty, nty, sum);
+        else if (act == FK_ACT_RELU)
+            stage_rows<T, FK_ACT_RELU>(a, i0, i1, col, ty, nty, sum);
+        else if (act == FK_ACT_GELU)
+            stage_rows<T, FK_ACT_GELU>(a, i0, i1, col, ty, nty, sum);
+        else
+            stage_rows<T, FK_ACT_SILU>(a, i0, i1, col, ty, nty, sum);
+    }
     if (a.colpart == nullptr) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) red[threadIdx.x][j] = sum[j];
+    for (int j = 0; j < 4; ++j) split(sum[j], red[threadIdx.x][2 * j], red[threadIdx.x][2 * j + 1]);
     __syncthreads();
     // thread c sums column c of the block over the ty row threads, in order
     for (int c = threadIdx.x; c < 8 * a.tx; c += 256) {
-        const int64_t cc = static_cast<int64_t>(blockIdx.x) * a.tx * 8 + c;
+        const int64_t cc = static_cast<int64_t>(bx) * a.tx * 8 + c;
         if (cc >= a.cols) continue;
         float s = 0.f;
         for (int y = 0; y < nty; ++y) s += red[y * a.tx + c / 8][c % 8];
-        a.colpart[static_cast<int64_t>(blockIdx.y) * a.cols + cc] = s;
+        a.colpart[static_cast<int64_t>(by) * a.cols + cc] = s;
     }
 }
 
@@ -143,30 +206,45 @@ __global__ void __launch_bounds__(1024)
     if (x == 0 && o < cols) db[o] = s;
 }
 
+// Threads across a row, 8 columns each: whole rows where they fit (memory likes long runs: at
+// 4096 bf16 columns, 4 KB of a row at a time and four rows ahead take 275 us where 512 bytes
+// and two rows took 447, 65,536 rows with GELU's slope, 1.6 GB).
 int stage_tx(int cols) {
     int tx = 1;
-    while (tx < 32 && tx * 8 < cols) tx *= 2;
+    while (tx < 256 && tx * 8 < cols) tx *= 2;
     return tx;
 }
 
-// Runs of rows the staging kernel is cut into: about six blocks an SM, each thread at
-// least one row.
+// Runs of rows the staging kernel is cut into: up to about six blocks an SM with four rows or
+// more a thread, or two an SM with fewer.
 int stage_parts(int64_t rows, int cols) {
-    const int tx = stage_tx(cols);
+    const int tx = stage_tx(cols), ty = 256 / tx;
     const int64_t bx = ceil_div(cols, tx * 8);
-    int64_t p = 148 * 6 / bx;
-    const int64_t most = ceil_div(rows, 256 / tx);
-    if (p > most) p = most;
+    auto up_to = [&](int64_t blocks, int64_t per_thread) {
+        const int64_t p = blocks / bx, most = ceil_div(rows, per_thread * ty);
+        return p < most ? p : most;
+    };
+    const int64_t wide = up_to(148 * 6, 4), narrow = up_to(148 * 2, 1);
+    const int64_t p = wide > narrow ? wide : narrow;
     return static_cast<int>(p < 1 ? 1 : p);
 }
 
-template <typename T>
-cudaError_t launch_stage(StageArgs a, cudaStream_t st) {
+void add_job(StageJobs &jobs, StageJob a) {
     a.tx = stage_tx(a.cols);
     a.vec = a.cols % 8 == 0 && aligned(a.src, 16) && aligned(a.Z, 16);
-    const dim3 grid(static_cast<unsigned>(ceil_div(a.cols, a.tx * 8)),
-                    static_cast<unsigned>(stage_parts(a.rows, a.cols)));
-    const cudaError_t e = launch_pdl(stage_kernel<T>, grid, dim3(256), 0, st, a);
+    a.gx = static_cast<int>(ceil_div(a.cols, a.tx * 8));
+    a.parts = stage_parts(a.rows, a.cols);
+    jobs.job[jobs.n] = a;
+    jobs.first[jobs.n + 1] = jobs.first[jobs.n] + a.gx * a.parts;
+    ++jobs.n;
+}
+
+template <typename T>
+cudaError_t launch_stage(const StageJobs &jobs, cudaStream_t st) {
+    if (jobs.n == 0) return cudaSuccess;
+    const cudaError_t e = launch_pdl(stage_kernel<T>,
+                                     dim3(static_cast<unsigned>(jobs.first[jobs.n])), dim3(256), 0,
+                                     st, jobs);
     if (e == cudaSuccess) note_launch();
     return e;
 }
@@ -324,11 +402,11 @@ LinearLayout linear_layout(int64_t N, int d, int m, fk_dtype dtype, bool backwar
     if (backward) {
         L.g = take(2 * L.planes * N * L.ldm);
         L.col = take(sizeof(float) * static_cast<int64_t>(stage_parts(N, m)) * m);
-        part = gemm_part_bytes(N, d, gemm_plan(N, d, m, L.planes));
-        const size_t q = gemm_part_bytes(m, d, gemm_plan(m, d, N, L.planes));
+        part = gemm_part_bytes(gemm_plan(N, d, m, L.planes));
+        const size_t q = gemm_part_bytes(gemm_plan(m, d, N, L.planes));
         part = part > q ? part : q;
     } else if (!few) {
-        part = gemm_part_bytes(N, m, gemm_plan(N, m, d, L.planes));
+        part = gemm_part_bytes(gemm_plan(N, m, d, L.planes));
     }
     L.part = take(static_cast<int64_t>(part));
     L.total = o;
@@ -336,24 +414,18 @@ LinearLayout linear_layout(int64_t N, int d, int m, fk_dtype dtype, bool backwar
 }
 
 // An operand of `rows` x `cols` as the tensor cores can read it: staged into `space` where
-// its type or row length asks for it.  `ld` receives its row length.
-template <typename T>
-cudaError_t operand(const void *src, int64_t rows, int cols, bool stage, uint16_t *space,
-                    cudaStream_t st, const uint16_t **base, int64_t *ld) {
-    if (!stage) {
-        *base = static_cast<const uint16_t *>(src);
-        *ld = cols;
-        return cudaSuccess;
-    }
-    *base = space;
-    *ld = round_up(cols, 8);
-    StageArgs s{};
+// its type or row length asks for it.
+GemmOperand operand(StageJobs &jobs, const void *src, int64_t rows, int cols, bool stage,
+                    uint16_t *space, bool mn_major) {
+    if (!stage) return GemmOperand{static_cast<const uint16_t *>(src), cols, mn_major};
+    StageJob s{};
     s.src = src;
     s.rows = rows;
     s.cols = cols;
     s.out = space;
-    s.ld = *ld;
-    return launch_stage<T>(s, st);
+    s.ld = round_up(cols, 8);
+    add_job(jobs, s);
+    return GemmOperand{space, s.ld, mn_major};
 }
 
 // One product: on the tensor cores, or (bf16 operands off 16-byte boundaries) without them.
@@ -382,11 +454,10 @@ cudaError_t linear_t(const LinearArgs &a, void *ws, cudaStream_t st) {
     if (a.N <= kFewRows) return launch_few_rows<T>(a, st);
     const LinearLayout L = linear_layout(a.N, a.d, a.m, a.dtype, false);
     GemmArgs g{};
-    cudaError_t e = operand<T>(a.X, a.N, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.x), st,
-                               &g.A.base, &g.A.ld);
-    if (e == cudaSuccess)
-        e = operand<T>(a.W, a.m, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.w), st, &g.B.base,
-                       &g.B.ld);
+    StageJobs jobs{};
+    g.A = operand(jobs, a.X, a.N, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.x), false);
+    g.B = operand(jobs, a.W, a.m, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.w), false);
+    const cudaError_t e = launch_stage<T>(jobs, st);
     if (e != cudaSuccess) return e;
     g.dtype = a.dtype;
     g.planes = L.planes;
@@ -412,13 +483,13 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
         if (e == cudaSuccess && a.db) e = cudaMemsetAsync(a.db, 0, sizeof(float) * a.m, st);
         return e;
     }
-    // G, and its column sums from the values before they are rounded to an operand
-    GemmOperand G{};
-    cudaError_t e = cudaSuccess;
+    // G, with its column sums from the values before they are rounded to an operand, and the
+    // other operands: one launch
+    StageJobs jobs{};
     const bool products = a.dX != nullptr || a.dW != nullptr;
     const bool write = products && (L.stage_m || a.act != FK_ACT_NONE);
     if (write || a.db) {
-        StageArgs s{};
+        StageJob s{};
         s.src = a.dY;
         s.Z = a.act != FK_ACT_NONE ? a.Zin : nullptr;
         s.rows = a.N;
@@ -427,17 +498,19 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
         s.out = write ? ws_ptr<uint16_t>(ws, L.g) : nullptr;
         s.ld = L.ldm;
         s.colpart = a.db ? ws_ptr<float>(ws, L.col) : nullptr;
-        if ((e = launch_stage<T>(s, st)) != cudaSuccess) return e;
+        add_job(jobs, s);
     }
+    GemmOperand W{}, X{};
+    if (a.dX) W = operand(jobs, a.W, a.m, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.w), true);
+    if (a.dW) X = operand(jobs, a.X, a.N, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.x), true);
+    cudaError_t e = launch_stage<T>(jobs, st);
+    if (e != cudaSuccess) return e;
     if (a.db) {
         e = launch_pdl(col_join_kernel, dim3(static_cast<unsigned>(ceil_div(a.m, 32))), dim3(1024),
                        0, st, ws_ptr<const float>(ws, L.col), stage_parts(a.N, a.m), a.m, a.db);
         if (e != cudaSuccess) return e;
         note_launch();
     }
-    if (!products) return e;
-    G.base = write ? ws_ptr<uint16_t>(ws, L.g) : static_cast<const uint16_t *>(a.dY);
-    G.ld = write ? L.ldm : a.m;
     GemmArgs g{};
     g.dtype = a.dtype;
     g.planes = L.planes;
@@ -445,26 +518,22 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
     g.cols = a.d;
     g.part = ws_ptr<float>(ws, L.part);
     g.err = ws_ptr<uint32_t>(ws, 0);
-    g.B.mn_major = true;
+    g.A.base = write ? ws_ptr<uint16_t>(ws, L.g) : static_cast<const uint16_t *>(a.dY);
+    g.A.ld = write ? L.ldm : a.m;
     if (a.dX) {
-        g.A = G;
-        e = operand<T>(a.W, a.m, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.w), st, &g.B.base,
-                       &g.B.ld);
+        g.B = W;
         g.rows = a.N;
         g.depth = a.m;
         g.C = a.dX;
-        if (e == cudaSuccess) e = product(g, st);
-        if (e != cudaSuccess) return e;
+        if ((e = product(g, st)) != cudaSuccess) return e;
     }
     if (a.dW) {
-        g.A = G;
         g.A.mn_major = true;
-        e = operand<T>(a.X, a.N, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.x), st, &g.B.base,
-                       &g.B.ld);
+        g.B = X;
         g.rows = a.m;
         g.depth = a.N;
         g.C = a.dW;
-        if (e == cudaSuccess) e = product(g, st);
+        e = product(g, st);
     }
     return e;
 }
