@@ -103,14 +103,33 @@ struct LossArgs {
     double *part;
 };
 
-// n, 1 / (n top) and coef scale K / n.
+// n, 1 / (n top) and coef scale K / n; and the least count.  A share f_k is worked with as its
+// distance from the least one, (counts_k - least) / (n top), exact before its one rounding:
+// f_j - t_i is then formed from numbers no larger than f_j and t_i, and is 0 where all counts
+// are the same.  t_i is the weighted mean of these plus the least share, as p sums to 1.
+// Called by the whole block.
 struct LossScales {
     float n, unit, gc;
-    __device__ __forceinline__ explicit LossScales(const LossArgs &a) {
+    int32_t least;
+    __device__ __forceinline__ LossScales(const LossArgs &a, int32_t *warps) {
         const int32_t r = *a.rows;
         n = static_cast<float>(r > 0 ? r : 1);
         unit = 1.f / (n * static_cast<float>(a.top));
         gc = a.coef * a.scale * static_cast<float>(a.K) / n;
+        least = 0x7fffffff;
+        for (int64_t k = threadIdx.x; k < a.K; k += kThreads) least = min(least, a.counts[k]);
+        least = __reduce_min_sync(0xffffffffu, least);
+        if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = least;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) least = min(least, warps[w]);
+    }
+    __device__ __forceinline__ float share(int32_t count) const {
+        return static_cast<float>(count - least) * unit;
+    }
+    // t_i from its part t and whether the row has any finite score
+    __device__ __forceinline__ float whole(float t, bool some) const {
+        return some ? t + static_cast<float>(least) * unit : 0.f;
     }
 };
 
@@ -264,10 +283,11 @@ __global__ void __launch_bounds__(kThreads, 3)
     };
     if (threadIdx.x == 0)
         for (int s = 0; s < stages; ++s) bring(first + s * step, s);
-    const LossScales c(a);
+    __shared__ int32_t least[kThreads / 32];
+    const LossScales c(a, least);
     for (int k = threadIdx.x; k < a.K; k += kThreads) {
         const int v = k / V, q = (v / TPR * (H / 2) + k % V / 4) * TPR + v % TPR;
-        reinterpret_cast<float *>(f + q)[k % 4] = static_cast<float>(a.counts[k]) * c.unit;
+        reinterpret_cast<float *>(f + q)[k % 4] = c.share(a.counts[k]);
     }
     __syncthreads();
     const float scale2 = a.scale * 1.44269504f;
@@ -347,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         }
         const float inv = s.m == -INFINITY ? 0.f : rcp_fast(s.z);
         const float ti = s.t * inv;
-        if (t == 0 && on) total += ti;
+        if (t == 0 && on) total += c.whole(ti, s.m != -INFINITY);
         if (dS == nullptr || i >= a.N) continue;
         // this warp's exponentials against the group's maximum, over the sum
         const float gp = TPR > 32 ? c.gc * exp2_fast(scale2 * (m - soft_base(s.m))) * inv
@@ -385,7 +405,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     pdl_trigger();
     constexpr int G = kThreads / TPR;
     const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-    const LossScales c(a);
+    __shared__ int32_t least[kThreads / 32];
+    const LossScales c(a, least);
     const float scale2 = a.scale * 1.44269504f;
     double total = 0.0;
     int slot = 0;
@@ -421,13 +442,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int j = n * TPR + t;
             e[n] = exp2_fast(scale2 * (e[n] - base));
             s.z += e[n];
-            if (j < a.K) s.t += e[n] * (static_cast<float>(a.counts[j]) * c.unit);
+            if (j < a.K) s.t += e[n] * c.share(a.counts[j]);
         }
         s = join_group<TPR>(s, scale2, red, slot);
         slot ^= 1;
         const float inv = s.m == -INFINITY ? 0.f : rcp_fast(s.z);
         const float ti = s.t * inv;
-        if (t == 0 && on) total += ti;
+        if (t == 0 && on) total += c.whole(ti, s.m != -INFINITY);
         if (dS != nullptr && i < a.N) {
             const float gp = TPR > 32 ? c.gc * exp2_fast(scale2 * (m - soft_base(s.m))) * inv
                                       : c.gc * inv;
@@ -436,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const int j = n * TPR + t;
                 if (j < a.K)
                     head_store(dS + i * a.K + j,
-                               e[n] * (static_cast<float>(a.counts[j]) * c.unit * gp - ti * gp));
+                               e[n] * gp * (c.share(a.counts[j]) - ti));
             }
         }
     }
@@ -452,7 +473,8 @@ __global__ void __launch_bounds__(kThreads)
     __shared__ double sums[kThreads];
     pdl_wait();
     pdl_trigger();
-    const LossScales c(a);
+    __shared__ int32_t least[kThreads / 32];
+    const LossScales c(a, least);
     const float scale2 = a.scale * 1.44269504f;
     double total = 0.0;
     int slot = 0;
@@ -471,18 +493,18 @@ __global__ void __launch_bounds__(kThreads)
         for (int64_t j = threadIdx.x; j < a.K; j += kThreads) {
             const float e = exp2_fast(scale2 * (head_load(s + j) - soft_base(r.m)));
             r.z += e;
-            r.t += e * (static_cast<float>(a.counts[j]) * c.unit);
+            r.t += e * c.share(a.counts[j]);
         }
         r = join_group<kThreads>(r, scale2, red, slot);
         slot ^= 1;
         const float inv = r.m == -INFINITY ? 0.f : 1.f / r.z;
         const float ti = r.t * inv;
-        if (threadIdx.x == 0) total += ti;
+        if (threadIdx.x == 0) total += c.whole(ti, r.m != -INFINITY);
         if (dS)
             for (int64_t j = threadIdx.x; j < a.K; j += kThreads) {
                 const float p = exp2_fast(scale2 * (head_load(s + j) - soft_base(r.m))) * inv;
                 head_store(dS + i * a.K + j,
-                           c.gc * p * (static_cast<float>(a.counts[j]) * c.unit - ti));
+                           c.gc * p * (c.share(a.counts[j]) - ti));
             }
     }
     finish_block(a, c, total, threadIdx.x == 0, sums);

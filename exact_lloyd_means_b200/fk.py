@@ -178,8 +178,8 @@ def _opt(t, name, dtype=None, shape=None):
 
 
 def _stream(stream) -> int:
-    if stream is None:  # the current stream's handle, without making a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -542,9 +542,12 @@ def _home(t: torch.Tensor, name: str, dims: int = 2) -> int:
 
 
 def _ptr(t, name: str, dtype, shape, dev: int) -> int:
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == dev and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _dev(t, name, dtype, shape)
     raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
 
@@ -554,11 +557,13 @@ def _ptr_or_none(t, name: str, dtype, shape, dev: int):
 
 
 def _space(ws, dev: int) -> int:
-    if (isinstance(ws, torch.Tensor) and ws.dtype is _u8 and ws.get_device() == dev
-            and ws.is_contiguous()):
-        return ws.data_ptr()
-    _dev(ws, "ws", _u8)
-    raise ValueError(f"ws must be on cuda:{dev}, got {ws.device}")
+    return _ptr(ws, "ws", _u8, ws.shape if isinstance(ws, torch.Tensor) else None, dev)
+
+
+def _stream_on(stream, dev: int) -> int:
+    if stream is None:  # the current stream's handle, without making a Stream object
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _point_code(dtype) -> int:
@@ -594,8 +599,9 @@ def fk_layer_norm(X: torch.Tensor, gamma: torch.Tensor | None, beta: torch.Tenso
                            _ptr_or_none(beta, "beta", _f32, (d,), dev), eps,
                            _ptr(Y, "Y", t, shape, dev),
                            _ptr_or_none(mean, "mean", _f32, (N,), dev),
-                           _ptr_or_none(rstd, "rstd", _f32, (N,), dev), _stream(stream))
-    _check(s, "fk_layer_norm")
+                           _ptr_or_none(rstd, "rstd", _f32, (N,), dev), _stream_on(stream, dev))
+    if s:
+        raise FkError(s, "fk_layer_norm")
 
 
 def layer_norm_backward_workspace(N: int, d: int, dtype=torch.float32, device="cuda"):
@@ -621,8 +627,9 @@ def fk_layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tenso
                                     _ptr_or_none(dX, "dX", t, shape, dev),
                                     _ptr_or_none(dgamma, "dgamma", _f32, (d,), dev),
                                     _ptr_or_none(dbeta, "dbeta", _f32, (d,), dev),
-                                    _space(ws, dev), ws.numel(), _stream(stream))
-    _check(s, "fk_layer_norm_backward")
+                                    _space(ws, dev), ws.numel(), _stream_on(stream, dev))
+    if s:
+        raise FkError(s, "fk_layer_norm_backward")
 
 
 def linear_workspace(N: int, d: int, m: int, dtype=torch.float32, device="cuda"):
@@ -659,8 +666,9 @@ def fk_linear(X: torch.Tensor, W: torch.Tensor, Y: torch.Tensor, ws: torch.Tenso
                        _ptr_or_none(bias, "bias", _f32, (m,), dev), _activation(act),
                        _ptr_or_none(residual, "residual", t, out, dev),
                        _ptr(Y, "Y", t, out, dev), _ptr_or_none(Z, "Z", t, out, dev),
-                       _space(ws, dev), ws.numel(), _stream(stream))
-    _check(s, "fk_linear")
+                       _space(ws, dev), ws.numel(), _stream_on(stream, dev))
+    if s:
+        raise FkError(s, "fk_linear")
 
 
 def fk_linear_backward(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, ws: torch.Tensor,
@@ -679,8 +687,9 @@ def fk_linear_backward(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, ws: t
                                 _ptr_or_none(dX, "dX", t, shape, dev),
                                 _ptr_or_none(dW, "dW", t, (m, d), dev),
                                 _ptr_or_none(dbias, "dbias", _f32, (m,), dev),
-                                _space(ws, dev), ws.numel(), _stream(stream))
-    _check(s, "fk_linear_backward")
+                                _space(ws, dev), ws.numel(), _stream_on(stream, dev))
+    if s:
+        raise FkError(s, "fk_linear_backward")
 
 
 def _selection(labels, N=None):
@@ -701,8 +710,9 @@ def fk_balance_counts(labels: torch.Tensor, counts: torch.Tensor, rows: torch.Te
     K = counts.shape[0]
     s = _lib.fk_balance_counts(_ptr(labels, "labels", _i32, shape, dev), N, top, K,
                                _ptr(counts, "counts", _i32, (K,), dev),
-                               _ptr(rows, "rows", _i32, (1,), dev), _stream(stream))
-    _check(s, "fk_balance_counts")
+                               _ptr(rows, "rows", _i32, (1,), dev), _stream_on(stream, dev))
+    if s:
+        raise FkError(s, "fk_balance_counts")
 
 
 def balance_workspace(N: int, K: int, dtype=torch.float32, device="cuda"):
@@ -725,8 +735,9 @@ def fk_balance_loss(S: torch.Tensor, labels: torch.Tensor, counts: torch.Tensor,
                              _ptr(rows, "rows", _i32, (1,), dev), scale, coef,
                              _ptr(loss, "loss", _f32, (1,), dev),
                              _ptr_or_none(dS, "dS", t, shape, dev), _space(ws, dev),
-                             ws.numel(), _stream(stream))
-    _check(s, "fk_balance_loss")
+                             ws.numel(), _stream_on(stream, dev))
+    if s:
+        raise FkError(s, "fk_balance_loss")
 
 
 class IvfFlatIndex:

@@ -370,6 +370,24 @@ def test_balance(fk, N, K, top, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [1, 3, 8, 64, 129, 4096, 9000])
+def test_balance_of_an_even_selection_has_no_gradient(fk, K, dtype):
+    """Every cell selected equally often: f_j - t_i is 0 for every score, and exactly so."""
+    t = TYPES[dtype]
+    S = rnd((2 * K, K), t, 3, 2.0) if K <= 129 else rnd((K, K), t, 3, 2.0)
+    N = S.shape[0]
+    lab = (torch.arange(N, dtype=torch.int32, device="cuda") % K).reshape(N, 1)
+    counts = torch.empty(K, dtype=torch.int32, device="cuda")
+    rows = torch.empty(1, dtype=torch.int32, device="cuda")
+    fk.fk_balance_counts(lab, counts, rows)
+    assert int(counts.min()) == int(counts.max()) == N // K
+    loss, dS = torch.empty(1, device="cuda"), torch.full_like(S, 9.0)
+    fk.fk_balance_loss(S, lab, counts, rows, loss, dS, fk.balance_workspace(N, K, t))
+    assert torch.all(dS == 0)
+    assert abs(float(loss) - 1.0) <= 4 * U  # K (1 / K) to a few roundings
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("K", [5, 300, 5000])
 def test_balance_rows_that_masks_leave_empty(fk, K, dtype):
     t = TYPES[dtype]
