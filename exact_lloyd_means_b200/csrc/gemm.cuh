@@ -25,9 +25,8 @@ struct GemmPlan {
 };
 
 struct GemmArgs {
-    fk_dtype dtype;  // of R, C and Z
+    fk_dtype dtype;  // of R, C and Z; FK_F32: operands of three planes
     GemmOperand A, B;
-    int planes;  // 1, or 3 with the six products that keep fp32 accuracy
     int64_t rows;
     int64_t cols, depth;
     const float *bias;
@@ -38,7 +37,7 @@ struct GemmArgs {
     uint32_t *err;
 };
 
-GemmPlan gemm_plan(int64_t rows, int64_t cols, int64_t depth, int planes);
+GemmPlan gemm_plan(int64_t rows, int64_t cols, int64_t depth, fk_dtype dtype);
 inline size_t gemm_part_bytes(const GemmPlan &p) {
     return p.splits > 1 ? sizeof(float) * p.tail * p.splits * p.tile() : 0;
 }

@@ -15,8 +15,10 @@
 //     both are 128-byte-swizzled TMA boxes, and the MMA descriptors say which.  So the three
 //     products of a linear layer and its gradients read their operands as they lie;
 //   * fp32 operands come as three bf16 planes (x = x0 + x1 + x2, 8 bits each, exact).  Six
-//     of the nine products keep everything above 2^-24 of the result: the small ones come
-//     first, so that they are added before the accumulator has its full size;
+//     of the nine products keep everything above 2^-24 of the result.  A stage holds all the
+//     planes, each loaded once for its six products; x0 y0 goes into an accumulator of its
+//     own and the five small products into another, so that these are not rounded to the
+//     size of the sum, and the sum is rounded no more often than that of bf16 operands;
 //   * every wait is bounded; on expiry the CTA records the timeout and winds down.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -34,12 +36,19 @@ constexpr int kBandRows = 8;  // tiles of one column band that run side by side
 
 // OV = consecutive columns an epilogue thread writes at once: 32 or 16 bytes of them, or one
 // column, where rows of the outputs do not start on such boundaries.
-template <int CG, int BN, int OV>
+// The tensor cores cut what they add to an accumulator (about 2^-24 of the sum a step of 16,
+// always towards zero: 4.4e-6 of the result at a depth of 4096).  So fp32 products are
+// accumulated in runs of 256 of the depth, 2e-7 each, and the runs added to fp32 registers;
+// bf16 ones, whose result is rounded to 2^-9 anyway, up to 131,072 of the depth.
+constexpr int kRunChunks = 4;
+constexpr int kMaxBf16Chunks = 2048;
+
+template <int CG, int BN, int NP, int OV>
 struct GemmCfg {
-    static constexpr int kABytes = kBM * kBK * 2;
+    static constexpr int kABytes = kBM * kBK * 2;  // one plane
     static constexpr int kBRows = BN / CG;
     static constexpr int kBBytes = kBRows * kBK * 2;
-    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kStageBytes = NP * (kABytes + kBBytes);
     static constexpr int kEpiWarps = 8;
     static constexpr int kStageOut = OV == 1 ? 32 * 33 * 4 : 0;  // a warp's 32 x 32 fp32
     static constexpr int kBarBytes = 256;
@@ -48,30 +57,27 @@ struct GemmCfg {
     static constexpr int kSmemBytes =
         kStages * kStageBytes + kEpiWarps * kStageOut + kBarBytes + 1024;
     static constexpr int kThreads = 64 + kEpiWarps * 32;
-    static constexpr int kTmemCols = 2 * BN;
+    static constexpr int kAccCols = NP == 3 ? 2 * BN : BN;  // of one tile
+    static constexpr int kTmemCols = 2 * kAccCols;
+    static_assert(kTmemCols <= 512 && kStages >= 2, "two tiles, two stages");
     static constexpr int kGroupCols = BN / (kEpiWarps / 4);  // columns of one epilogue group
     static_assert(kSmemBytes <= 232448, "shared memory");
     static_assert(kStageBytes % 1024 == 0, "stage bases stay 1024-byte aligned");
     static_assert(8 * (2 * kStages + 5) + 8 <= kBarBytes, "barriers");
 };
 
+// Planes of an operand of type T.
+template <typename T>
+constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+
 struct GemmShape {
     int64_t rows, cols;
     int nkc;      // chunks of 64 in the depth
     int splits;
-    int terms;    // products per chunk: 1, or 6 of three planes
     int a_mn, b_mn;
     int64_t tiles_r, tiles_c, units;
     int64_t full, tail;  // tiles with the whole depth, tiles with their depth cut
 };
-
-// The plane of A and of B in product t of the six.
-__device__ __forceinline__ int term_a(int terms, int t) {
-    return terms == 1 ? 0 : (0x010210 >> (4 * t)) & 3;  // 0 1 2 0 1 0
-}
-__device__ __forceinline__ int term_b(int terms, int t) {
-    return terms == 1 ? 0 : (0x001012 >> (4 * t)) & 3;  // 2 1 0 1 0 0
-}
 
 // Tile t in the order of work: bands of kBandRows row tiles, rows fastest within a band, so that
 // the tiles running side by side share their operands in L2.
@@ -116,11 +122,12 @@ __device__ __forceinline__ void gemm_timeout(volatile uint32_t *abort_flag, uint
 }
 
 template <int CG, int BN, typename T, int OV>
-__global__ void __launch_bounds__(GemmCfg<CG, BN, OV>::kThreads, 1)
+__global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const GemmShape sh, const Epilogue ep, int bvec, float *__restrict__ part,
                 uint32_t *__restrict__ err, uint64_t wait_ns) {
-    using Cfg = GemmCfg<CG, BN, OV>;
+    constexpr int NP = kPlanes<T>;
+    using Cfg = GemmCfg<CG, BN, NP, OV>;
     constexpr int S = Cfg::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -183,44 +190,44 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, OV>::kThreads, 1)
                 const Unit un = unit_of(sh, u);
                 const int r0 = static_cast<int>(un.tr * (kBM * CG) + rank * kBM);
                 const int c0 = static_cast<int>(un.tc * BN + rank * Cfg::kBRows);
-                for (int t = 0; t < sh.terms && ok; ++t) {
-                    const int pa = term_a(sh.terms, t), pb = term_b(sh.terms, t);
-                    for (int kc = un.k0; kc < un.k1; ++kc) {
-                        if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag, wait_ns)) {
-                            gemm_timeout(abort_flag, err);
-                            ok = false;
-                            break;
-                        }
-                        if (rank == 0)
-                            ptx::mbar_arrive_expect_tx(&full[stage], CG * Cfg::kStageBytes);
-                        uint8_t *sa = smem + stage * Cfg::kStageBytes;
-                        uint8_t *sb = sa + Cfg::kABytes;
-                        const int k = kc * kBK;
-                        auto load = [&](uint8_t *dst, const CUtensorMap *map, int x, int y,
-                                        int p) {
-                            if constexpr (CG == 2)
-                                ptx::tma_load_3d_pair(dst, map, full_c + stage * 8, x, y, p);
-                            else
-                                ptx::tma_load_3d(dst, map, &full[stage], x, y, p);
-                        };
+                for (int kc = un.k0; kc < un.k1; ++kc) {
+                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag, wait_ns)) {
+                        gemm_timeout(abort_flag, err);
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0)
+                        ptx::mbar_arrive_expect_tx(&full[stage], CG * Cfg::kStageBytes);
+                    const int k = kc * kBK;
+                    auto load = [&](uint8_t *dst, const CUtensorMap *map, int x, int y, int p) {
+                        if constexpr (CG == 2)
+                            ptx::tma_load_3d_pair(dst, map, full_c + stage * 8, x, y, p);
+                        else
+                            ptx::tma_load_3d(dst, map, &full[stage], x, y, p);
+                    };
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) {
+                        uint8_t *sa = smem + stage * Cfg::kStageBytes + p * Cfg::kABytes;
+                        uint8_t *sb = smem + stage * Cfg::kStageBytes + NP * Cfg::kABytes +
+                                      p * Cfg::kBBytes;
                         if (sh.a_mn) {
 #pragma unroll
                             for (int b = 0; b < kBM / 64; ++b)
-                                load(sa + b * 8192, &tmA, r0 + b * 64, k, pa);
+                                load(sa + b * 8192, &tmA, r0 + b * 64, k, p);
                         } else {
-                            load(sa, &tmA, k, r0, pa);
+                            load(sa, &tmA, k, r0, p);
                         }
                         if (sh.b_mn) {
 #pragma unroll
                             for (int b = 0; b < Cfg::kBRows / 64; ++b)
-                                load(sb + b * 8192, &tmB, c0 + b * 64, k, pb);
+                                load(sb + b * 8192, &tmB, c0 + b * 64, k, p);
                         } else {
-                            load(sb, &tmB, k, c0, pb);
+                            load(sb, &tmB, k, c0, p);
                         }
-                        if (++stage == S) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
+                    }
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
             }
@@ -231,54 +238,70 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, OV>::kThreads, 1)
             const uint32_t idesc = ptx::idesc_bf16_f32(kBM * CG, BN) |
                                    ptx::idesc_mn_major(sh.a_mn != 0, sh.b_mn != 0);
             const uint64_t ka = sh.a_mn ? 2048 / 16 : 2, kb = sh.b_mn ? 2048 / 16 : 2;
+            // chunks of one accumulation
+            constexpr int kRun = NP == 3 ? kRunChunks : 0x40000000;
             uint32_t stage = 0, phase = 0, it = 0;
             bool ok = true;
-            for (int64_t u = first; u < sh.units && ok; u += step, ++it) {
+            for (int64_t u = first; u < sh.units && ok; u += step) {
                 const Unit un = unit_of(sh, u);
-                const uint32_t acc = it & 1u;
-                if (!ptx::mbar_wait(&tempty[acc], ((it >> 1) & 1u) ^ 1u, abort_flag, wait_ns)) {
-                    gemm_timeout(abort_flag, err);
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                const uint32_t dt = tmem + acc * BN;
-                const int n = sh.terms * (un.k1 - un.k0);
-                for (int i = 0; i < n; ++i) {
-                    if (!ptx::mbar_wait(&full[stage], phase, abort_flag, wait_ns)) {
+                for (int k0 = un.k0; k0 < un.k1 && ok; k0 += kRun, ++it) {
+                    const uint32_t acc = it & 1u;
+                    if (!ptx::mbar_wait(&tempty[acc], ((it >> 1) & 1u) ^ 1u, abort_flag, wait_ns)) {
                         gemm_timeout(abort_flag, err);
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint32_t sa = ptx::smem_u32(smem + stage * Cfg::kStageBytes);
-                    const uint32_t sb = sa + Cfg::kABytes;
-                    const uint64_t da = sh.a_mn ? ptx::sdesc_mn_sw128(sa)
-                                                : ptx::sdesc_k_sw128(sa);
-                    const uint64_t db = sh.b_mn ? ptx::sdesc_mn_sw128(sb)
-                                                : ptx::sdesc_k_sw128(sb);
+                    const uint32_t dt = tmem + acc * Cfg::kAccCols;
+                    const int n = un.k1 - k0 < kRun ? un.k1 - k0 : kRun;
+                    for (int i = 0; i < n; ++i) {
+                        if (!ptx::mbar_wait(&full[stage], phase, abort_flag, wait_ns)) {
+                            gemm_timeout(abort_flag, err);
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        const uint32_t sa = ptx::smem_u32(smem + stage * Cfg::kStageBytes);
+                        const uint32_t sb = sa + NP * Cfg::kABytes;
+                        const uint64_t da = sh.a_mn ? ptx::sdesc_mn_sw128(sa)
+                                                    : ptx::sdesc_k_sw128(sa);
+                        const uint64_t db = sh.b_mn ? ptx::sdesc_mn_sw128(sb)
+                                                    : ptx::sdesc_k_sw128(sb);
+                        auto mma = [&](uint32_t d, int pa, int pb, int ks, uint32_t more) {
+                            const uint64_t x = da + pa * (Cfg::kABytes / 16) + ks * ka;
+                            const uint64_t y = db + pb * (Cfg::kBBytes / 16) + ks * kb;
+                            if constexpr (CG == 2)
+                                ptx::mma_bf16_ss_pair(d, x, y, idesc, more);
+                            else
+                                ptx::mma_bf16_ss(d, x, y, idesc, more);
+                        };
 #pragma unroll
-                    for (int ks = 0; ks < kBK / 16; ++ks) {
-                        const uint32_t more = i > 0 || ks > 0 ? 1u : 0u;
+                        for (int ks = 0; ks < kBK / 16; ++ks) {
+                            const uint32_t more = i > 0 || ks > 0 ? 1u : 0u;
+                            mma(dt, 0, 0, ks, more);
+                            if constexpr (NP == 3) {
+                                mma(dt + BN, 0, 2, ks, more);
+                                mma(dt + BN, 1, 1, ks, 1u);
+                                mma(dt + BN, 2, 0, ks, 1u);
+                                mma(dt + BN, 0, 1, ks, 1u);
+                                mma(dt + BN, 1, 0, ks, 1u);
+                            }
+                        }
                         if constexpr (CG == 2)
-                            ptx::mma_bf16_ss_pair(dt, da + ks * ka, db + ks * kb, idesc, more);
+                            ptx::mma_commit_pair(&empty[stage], 0x3);
                         else
-                            ptx::mma_bf16_ss(dt, da + ks * ka, db + ks * kb, idesc, more);
+                            ptx::mma_commit(&empty[stage]);
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
+                    if (!ok) break;
                     if constexpr (CG == 2)
-                        ptx::mma_commit_pair(&empty[stage], 0x3);
+                        ptx::mma_commit_pair(&tfull[acc], 0x3);
                     else
-                        ptx::mma_commit(&empty[stage]);
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                        ptx::mma_commit(&tfull[acc]);
                 }
-                if (!ok) break;
-                if constexpr (CG == 2)
-                    ptx::mma_commit_pair(&tfull[acc], 0x3);
-                else
-                    ptx::mma_commit(&tfull[acc]);
             }
             if (!ok) {
                 if constexpr (CG == 2)
@@ -297,37 +320,16 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, OV>::kThreads, 1)
             reinterpret_cast<float *>(stage_out + (warp - 2) * Cfg::kStageOut);
         const uint32_t tempty_c =
             CG == 2 ? ptx::mapa_shared(ptx::smem_u32(tempty), 0) : 0u;
+        constexpr int C = Cfg::kGroupCols / 32;
         uint32_t it = 0;
-        for (int64_t u = first; u < sh.units; u += step, ++it) {
+        bool ok = true;
+        for (int64_t u = first; u < sh.units && ok; u += step) {
             const Unit un = unit_of(sh, u);
-            const uint32_t acc = it & 1u;
             const int64_t r0 = un.tr * (kBM * CG) + rank * kBM + q * 32;
             const int64_t c0 = un.tc * BN + g * Cfg::kGroupCols;
-            uint32_t good = 0;
-            if (lane == 0) good = ptx::mbar_wait(&tfull[acc], (it >> 1) & 1u, abort_flag, wait_ns);
-            if (!__shfl_sync(0xffffffffu, good, 0)) {
-                if (lane == 0) gemm_timeout(abort_flag, err);
-                break;
-            }
-            ptx::tc_fence_after();
-            const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN +
-                                g * Cfg::kGroupCols;
-#pragma unroll 1
-            for (int c = 0; c < Cfg::kGroupCols / 32; ++c) {
+            // columns c0 + 32 c .. + 31 of this thread's row, finished
+            auto finish = [&](int c, float (&v)[32]) {
                 const int64_t col = c0 + c * 32;
-                __syncwarp();
-                float v[32];
-                ptx::tmem_ld32_sync(tb + c * 32, v);
-                if (c == Cfg::kGroupCols / 32 - 1) {  // the accumulator is free again
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (CG == 2)
-                            ptx::mbar_arrive_cluster(tempty_c + acc * 8);
-                        else
-                            ptx::mbar_arrive(&tempty[acc]);
-                    }
-                }
                 if (un.part >= 0) {  // fp32 partial products, the whole tile
                     float *dst = part + (un.part * CG + rank) * (kBM * BN) +
                                  (q * 32 + lane) * BN + g * Cfg::kGroupCols + c * 32;
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, OV>::kThreads, 1)
                     for (int j = 0; j < 32; ++j) z[j / OV][j % OV] = v[j];
                     Pieces o{(r0 + lane) * sh.cols + col, OV, col, OV, 0u};
                     const int64_t left = (sh.cols - col) / OV;  // pieces before the last column
-                    if (r0 + lane >= sh.rows || left <= 0) continue;
+                    if (r0 + lane >= sh.rows || left <= 0) return;
                     if (left >= 32 / OV) {
                         epilogue_pieces<T, OV, true>(ep, o, bvec, z);
                     } else {
@@ -367,6 +369,71 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, OV>::kThreads, 1)
                     }
                     __syncwarp();
                 }
+            };
+            auto wait_acc = [&]() -> bool {
+                uint32_t good = 0;
+                if (lane == 0)
+                    good = ptx::mbar_wait(&tfull[it & 1u], (it >> 1) & 1u, abort_flag, wait_ns);
+                if (__shfl_sync(0xffffffffu, good, 0)) {
+                    ptx::tc_fence_after();
+                    return true;
+                }
+                if (lane == 0) gemm_timeout(abort_flag, err);
+                return false;
+            };
+            auto acc_cols = [&] {
+                return tmem + (static_cast<uint32_t>(q * 32) << 16) + (it & 1u) * Cfg::kAccCols +
+                       g * Cfg::kGroupCols;
+            };
+            auto release = [&] {  // the accumulator is free again
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2)
+                        ptx::mbar_arrive_cluster(tempty_c + (it & 1u) * 8);
+                    else
+                        ptx::mbar_arrive(&tempty[it & 1u]);
+                }
+            };
+            if constexpr (NP == 1) {
+                if (!(ok = wait_acc())) break;
+                const uint32_t tb = acc_cols();
+#pragma unroll 1
+                for (int c = 0; c < C; ++c) {
+                    __syncwarp();
+                    float v[32];
+                    ptx::tmem_ld32_sync(tb + c * 32, v);
+                    if (c == C - 1) release();
+                    finish(c, v);
+                }
+                ++it;
+            } else {
+                // run by run of the depth into registers, both accumulators of each
+                float sum[C][32];
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
+                for (int k = un.k0; k < un.k1; k += kRunChunks, ++it) {
+                    if (!(ok = wait_acc())) break;
+                    const uint32_t tb = acc_cols();
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        __syncwarp();
+                        float v[32];
+                        ptx::tmem_ld32_sync(tb + BN + c * 32, v);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[c][j] += v[j];
+                        __syncwarp();
+                        ptx::tmem_ld32_sync(tb + c * 32, v);
+                        if (c == C - 1) release();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[c][j] += v[j];
+                    }
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < C; ++c) finish(c, sum[c]);
             }
         }
     }
@@ -393,7 +460,7 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, OV>::kThreads, 1)
 }
 
 // Join the partial products of the tail tiles, in order, and apply the epilogue.  Block (x,
-// y): rows of tail tile y.
+// y): rows of tail tile x.
 template <typename T, int V>
 __global__ void __launch_bounds__(256)
     gemm_join_kernel(const float *__restrict__ part, const GemmShape s, int tile_rows, int bn,
@@ -401,11 +468,11 @@ __global__ void __launch_bounds__(256)
     pdl_wait();
     pdl_trigger();
     int64_t tr, tc;
-    tile_of(s, s.full + blockIdx.y, tr, tc);
+    tile_of(s, s.full + blockIdx.x, tr, tc);
     const int64_t size = static_cast<int64_t>(tile_rows) * bn;
-    const float *base = part + blockIdx.y * s.splits * size;
+    const float *base = part + static_cast<int64_t>(blockIdx.x) * s.splits * size;
     const int per_row = bn / V;
-    for (int t = blockIdx.x * 256 + threadIdx.x; t < tile_rows * per_row; t += gridDim.x * 256) {
+    for (int t = blockIdx.y * 256 + threadIdx.x; t < tile_rows * per_row; t += gridDim.y * 256) {
         const int lr = t / per_row, lc = (t - lr * per_row) * V;
         const int64_t row = tr * tile_rows + lr, col = tc * bn + lc;
         if (row >= s.rows || col >= s.cols) continue;
@@ -444,24 +511,23 @@ bool operand_map(CUtensorMap *m, const GemmOperand &o, int64_t outer, int64_t in
 
 template <int CG, int BN, typename T, int OV>
 cudaError_t launch_cfg(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
-    using Cfg = GemmCfg<CG, BN, OV>;
+    using Cfg = GemmCfg<CG, BN, kPlanes<T>, OV>;
     auto kernel = gemm_kernel<CG, BN, T, OV>;
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t e = smem_opt_in(kernel, Cfg::kSmemBytes, smem_set);
     if (e != cudaSuccess) return e;
     CUtensorMap tA, tB;
     const bool ok =
-        (a.A.mn_major ? operand_map(&tA, a.A, a.depth, a.rows, a.planes, 64)
-                      : operand_map(&tA, a.A, a.rows, a.depth, a.planes, kBM)) &&
-        (a.B.mn_major ? operand_map(&tB, a.B, a.depth, a.cols, a.planes, 64)
-                      : operand_map(&tB, a.B, a.cols, a.depth, a.planes, Cfg::kBRows));
+        (a.A.mn_major ? operand_map(&tA, a.A, a.depth, a.rows, kPlanes<T>, 64)
+                      : operand_map(&tA, a.A, a.rows, a.depth, kPlanes<T>, kBM)) &&
+        (a.B.mn_major ? operand_map(&tB, a.B, a.depth, a.cols, kPlanes<T>, 64)
+                      : operand_map(&tB, a.B, a.cols, a.depth, kPlanes<T>, Cfg::kBRows));
     if (!ok) return cudaErrorInvalidValue;
     GemmShape s{};
     s.rows = a.rows;
     s.cols = a.cols;
     s.nkc = static_cast<int>(ceil_div(a.depth, kBK));
     s.splits = p.splits;
-    s.terms = a.planes == 3 ? 6 : 1;
     s.a_mn = a.A.mn_major;
     s.b_mn = a.B.mn_major;
     s.tiles_r = ceil_div(a.rows, kBM * CG);
@@ -500,8 +566,8 @@ cudaError_t launch_cfg(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
         const int64_t want = ceil_div(static_cast<int64_t>(device_sm_count()) * 8, p.tail);
         const int64_t most = p.tile() / JV / 256;
         e = launch_pdl(gemm_join_kernel<T, JV>,
-                       dim3(static_cast<unsigned>(want < most ? want : most),
-                            static_cast<unsigned>(p.tail)),
+                       dim3(static_cast<unsigned>(p.tail),
+                            static_cast<unsigned>(want < most ? want : most)),
                        dim3(256), 0, st, static_cast<const float *>(a.part), s, kBM * CG, BN, ep,
                        bvec);
         if (e == cudaSuccess) note_launch();
@@ -511,7 +577,8 @@ cudaError_t launch_cfg(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
 
 template <typename T, int OV>
 cudaError_t launch_v(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
-    if (p.cg == 2) return launch_cfg<2, 256, T, OV>(a, p, st);
+    // (fp32: two accumulators a tile, so half the columns)
+    if (p.cg == 2) return launch_cfg<2, 256 / (kPlanes<T> == 3 ? 2 : 1), T, OV>(a, p, st);
     if (p.bn == 128) return launch_cfg<1, 128, T, OV>(a, p, st);
     return launch_cfg<1, 64, T, OV>(a, p, st);
 }
@@ -531,21 +598,27 @@ cudaError_t launch_t(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
 }  // namespace
 
 // The cheapest cut by a model in SM cycles: a chunk of 64 of the depth takes the time its
-// operands take to arrive (64 bytes a cycle and SM) or its products, whichever is longer: 512
-// for the pair's 256 x 256 tile, 512 for 128 x 128, 384 for 128 x 64; the ring fills and the
-// last accumulator empties once (about 4000).  Tiles run in waves of as many as the GPU
-// holds; those of the last, partial wave may have their depth cut so that it is spread over
-// the GPU, in parts of at least four chunks: that costs a launch (about 4000) and the partial
+// operands take to arrive (64 bytes a cycle and SM) or that of its products, whichever is
+// longer.  bf16: 512 for the pair's 256 x 256 tile, 512 for 128 x 128, 384 for 128 x 64; three
+// planes: 1536 for 256 x 128 and for 128 x 128, 1152 for 128 x 64.  The ring fills and the last
+// accumulator empties once (about 4000).  Tiles run in waves of as many as the GPU holds;
+// those of the last, partial wave may have their depth cut so that it is spread over the
+// GPU, in parts of at least four chunks: that costs a launch (about 4000) and the partial
 // products' way through L2 (about 3000 bytes a cycle).
-GemmPlan gemm_plan(int64_t rows, int64_t cols, int64_t depth, int planes) {
+GemmPlan gemm_plan(int64_t rows, int64_t cols, int64_t depth, fk_dtype dtype) {
     const int64_t nkc = ceil_div(depth, kBK);
-    const int terms = planes == 3 ? 6 : 1;
-    static constexpr struct {
+    struct Choice {
         int cg, bn, cycles;
-    } kCfg[3] = {{2, 256, 512}, {1, 128, 512}, {1, 64, 384}};
+    };
+    static constexpr Choice kBf16[3] = {{2, 256, 512}, {1, 128, 512}, {1, 64, 384}};
+    static constexpr Choice kF32[3] = {{2, 128, 1536}, {1, 128, 1536}, {1, 64, 1152}};
     GemmPlan best{};
+    if (dtype == FK_BF16 && nkc > kMaxBf16Chunks) {  // every tile's depth in parts
+        const int64_t tiles = ceil_div(rows, 256) * ceil_div(cols, 256);
+        return GemmPlan{2, 256, static_cast<int>(ceil_div(nkc, kMaxBf16Chunks)), 0, tiles};
+    }
     double best_cost = -1;
-    for (const auto &c : kCfg) {
+    for (const Choice &c : dtype == FK_F32 ? kF32 : kBf16) {
         const int64_t tiles = ceil_div(rows, kBM * c.cg) * ceil_div(cols, c.bn);
         const int64_t slots = 148 / c.cg;
         GemmPlan p{c.cg, c.bn, 1, tiles / slots * slots, tiles % slots};
@@ -554,7 +627,7 @@ GemmPlan gemm_plan(int64_t rows, int64_t cols, int64_t depth, int planes) {
             const double waves = static_cast<double>(p.full / slots);
             const double last = static_cast<double>(ceil_div(p.tail * p.splits, slots));
             double cost = 4000 + (waves + last) * 500 +
-                          (waves * nkc + last * ceil_div(nkc, p.splits)) * terms * c.cycles;
+                          (waves * nkc + last * ceil_div(nkc, p.splits)) * c.cycles;
             if (p.splits > 1)
                 cost += 4000 + 8.0 * static_cast<double>(p.tail * p.splits * p.tile()) / 3000;
             if (best_cost < 0 || cost < best_cost) {

@@ -402,11 +402,11 @@ LinearLayout linear_layout(int64_t N, int d, int m, fk_dtype dtype, bool backwar
     if (backward) {
         L.g = take(2 * L.planes * N * L.ldm);
         L.col = take(sizeof(float) * static_cast<int64_t>(stage_parts(N, m)) * m);
-        part = gemm_part_bytes(gemm_plan(N, d, m, L.planes));
-        const size_t q = gemm_part_bytes(gemm_plan(m, d, N, L.planes));
+        part = gemm_part_bytes(gemm_plan(N, d, m, dtype));
+        const size_t q = gemm_part_bytes(gemm_plan(m, d, N, dtype));
         part = part > q ? part : q;
     } else if (!few) {
-        part = gemm_part_bytes(gemm_plan(N, m, d, L.planes));
+        part = gemm_part_bytes(gemm_plan(N, m, d, dtype));
     }
     L.part = take(static_cast<int64_t>(part));
     L.total = o;
@@ -431,7 +431,7 @@ GemmOperand operand(StageJobs &jobs, const void *src, int64_t rows, int cols, bo
 // One product: on the tensor cores, or (bf16 operands off 16-byte boundaries) without them.
 cudaError_t product(const GemmArgs &a, cudaStream_t st) {
     if (aligned(a.A.base, 16) && aligned(a.B.base, 16))
-        return launch_gemm(a, gemm_plan(a.rows, a.cols, a.depth, a.planes), st);
+        return launch_gemm(a, gemm_plan(a.rows, a.cols, a.depth, a.dtype), st);
     Epilogue ep{};
     ep.bias = a.bias;
     ep.R = a.R;
@@ -460,7 +460,6 @@ cudaError_t linear_t(const LinearArgs &a, void *ws, cudaStream_t st) {
     const cudaError_t e = launch_stage<T>(jobs, st);
     if (e != cudaSuccess) return e;
     g.dtype = a.dtype;
-    g.planes = L.planes;
     g.rows = a.N;
     g.cols = a.m;
     g.depth = a.d;
@@ -488,6 +487,7 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
     StageJobs jobs{};
     const bool products = a.dX != nullptr || a.dW != nullptr;
     const bool write = products && (L.stage_m || a.act != FK_ACT_NONE);
+    bool join = false;
     if (write || a.db) {
         StageJob s{};
         s.src = a.dY;
@@ -497,7 +497,9 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
         s.act = a.act;
         s.out = write ? ws_ptr<uint16_t>(ws, L.g) : nullptr;
         s.ld = L.ldm;
-        s.colpart = a.db ? ws_ptr<float>(ws, L.col) : nullptr;
+        // a single run of rows has the sums themselves
+        join = a.db && stage_parts(a.N, a.m) > 1;
+        s.colpart = join ? ws_ptr<float>(ws, L.col) : a.db;
         add_job(jobs, s);
     }
     GemmOperand W{}, X{};
@@ -505,7 +507,7 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
     if (a.dW) X = operand(jobs, a.X, a.N, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.x), true);
     cudaError_t e = launch_stage<T>(jobs, st);
     if (e != cudaSuccess) return e;
-    if (a.db) {
+    if (join) {
         e = launch_pdl(col_join_kernel, dim3(static_cast<unsigned>(ceil_div(a.m, 32))), dim3(1024),
                        0, st, ws_ptr<const float>(ws, L.col), stage_parts(a.N, a.m), a.m, a.db);
         if (e != cudaSuccess) return e;
@@ -513,7 +515,6 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
     }
     GemmArgs g{};
     g.dtype = a.dtype;
-    g.planes = L.planes;
     g.act = FK_ACT_NONE;
     g.cols = a.d;
     g.part = ws_ptr<float>(ws, L.part);

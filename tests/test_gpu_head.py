@@ -268,6 +268,49 @@ def test_linear_backward(fk, N, d, m, dtype):
     assert fk.fk_get_device_error(ws) == fk.FK_OK
 
 
+@pytest.mark.parametrize("depth", [64, 700, 4096, 40000])
+def test_linear_fp32_error_does_not_grow_with_the_depth(fk, depth):
+    """Sums of `depth` products of fp32 numbers, in both passes.  The accumulator of the tensor
+    cores cuts at most 2^-23 of the sum at each of the 16 steps of a run of 256 (and of the few
+    steps that lead up to it); the runs are added with rounding to nearest.  With the running
+    sum averaging half its end, that is 16 2^-24 = 9.5e-7 if every cut were the largest; half
+    of that on average, and the runs' own signs and the plain roundings well inside the rest."""
+    N, m = 96, 80
+    g = torch.Generator(device="cuda").manual_seed(depth)
+    A = torch.randn((N, depth), generator=g, device="cuda")
+    B = torch.randn((m, depth), generator=g, device="cuda")
+
+    def off(got, want):
+        return float((got.double() - want).norm() / want.norm())
+
+    Y = torch.empty((N, m), device="cuda")
+    fk.fk_linear(A, B, Y, fk.linear_workspace(N, depth, m))
+    want = A.double() @ B.double().t()
+    assert off(Y, want) <= 9.5e-7
+    # dX over the outputs, dW over the rows
+    dX = torch.empty((N, m), device="cuda")
+    fk.fk_linear_backward(A, torch.zeros((N, m), device="cuda"), B.t().contiguous(),
+                          fk.linear_backward_workspace(N, m, depth), dX=dX)
+    assert off(dX, want) <= 9.5e-7
+    dW = torch.empty((N, m), device="cuda")
+    At, Bt = A.t().contiguous(), B.t().contiguous()
+    fk.fk_linear_backward(At, Bt, torch.zeros((N, m), device="cuda"),
+                          fk.linear_backward_workspace(depth, m, N), dW=dW)
+    assert off(dW, want) <= 9.5e-7
+
+
+def test_linear_bf16_over_a_very_long_depth(fk):
+    """A gradient over 300,000 rows: the depth is cut into parts, and the error stays that of
+    one rounding to bf16 (2^-8 at most, a third of that on average)."""
+    N, d, m = 300_001, 24, 40
+    X, dY = rnd((N, d), torch.bfloat16, 1, shift=0.1), rnd((N, m), torch.bfloat16, 2, shift=0.1)
+    W = rnd((m, d), torch.bfloat16, 3)
+    dW = torch.empty_like(W)
+    fk.fk_linear_backward(dY, X, W, fk.linear_backward_workspace(N, d, m, torch.bfloat16), dW=dW)
+    want = dY.double().t() @ X.double()
+    assert float(((dW.double() - want).abs() / want.abs()).max()) <= half_step(torch.bfloat16) * 1.1
+
+
 def test_linear_fp32_keeps_every_bit_of_its_operands(fk):
     """One-term sums: the product of two fp32 numbers to fp32 accuracy, over a wide range of
     exponents."""
