@@ -89,7 +89,7 @@ __global__ void balance_zero_kernel(int32_t *__restrict__ counts, int K,
                                     int32_t *__restrict__ rows) {
     pdl_wait();
     pdl_trigger();
-    for (int k = blockIdx.x * blockDim.x + threadIdx.x; k < K; k += gridDim.x * blockDim.x)
+    for (int64_t k = blockIdx.x * blockDim.x + threadIdx.x; k < K; k += gridDim.x * blockDim.x)
         counts[k] = 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) *rows = 0;
 }

@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(128)
     float s[NR] = {};
     if (vec) {
 #pragma unroll 4
-        for (int k = lane * V; k < d; k += 32 * V) {
+        for (int64_t k = lane * V; k < d; k += 32 * V) {
             float a[V];
             unpack16(*reinterpret_cast<const uint4 *>(w + k), a);
 #pragma unroll
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(128)
         }
     } else {
 #pragma unroll 4
-        for (int k = lane; k < d; k += 32) {
+        for (int64_t k = lane; k < d; k += 32) {
             const float a = head_load(w + k);
 #pragma unroll
             for (int r = 0; r < NR; ++r)

@@ -402,8 +402,9 @@ FK_API fk_status fk_ivf_search(const float *Q, int64_t nq, int d, const float *C
  * Common to all of them:
  *   - points and matrices are FK_F32 or FK_BF16, row-major and contiguous; vectors (bias,
  *     gamma, beta and their gradients, mean, rstd) are fp32, as centroids are;
- *   - any d, m, K >= 1 and 0 <= N < 2^31, element-aligned pointers (16-byte aligned rows are
- *     faster); N = 0 writes no row, and gradients that are sums over rows become 0;
+ *   - any d, m, K >= 1 and 0 <= N < 2^31, matrices of at most 2^46 elements, element-aligned
+ *     pointers (16-byte aligned rows are faster, for bf16 products by far); N = 0 writes no
+ *     row, and gradients that are sums over rows become 0;
  *   - products, statistics and sums are accumulated in fp32 or more and every output is
  *     rounded once; no floating-point atomics, so results repeat bit for bit;
  *   - outputs overlap neither an input nor one another, except where "may be" says so
@@ -451,7 +452,12 @@ FK_API fk_status fk_linear_backward_workspace_size(int64_t N, int d, int m, fk_d
  * X: N x d, W: m x d (one row per output, like centroids), bias: m floats or NULL,
  * residual: N x m or NULL, Y: N x m (may be residual), Z: N x m, optional: the
  * pre-activation, which the backward pass needs when act is not FK_ACT_NONE.
- * With W = C and bias = -||c||^2 / 2 it scores points against every centroid. */
+ * With W = C and bias = -||c||^2 / 2 it scores points against every centroid.
+ * Precision: FK_BF16 products are exact, accumulated in fp32, and the outputs rounded once.
+ * FK_F32 operands are taken as three bf16 numbers each, with the six products that matter to
+ * fp32; the sums are within about 2^-22 of the result at any depth.  fp32 values below about
+ * 2^-110 lose their lowest bits, and where an operand is infinite a result may be NaN instead
+ * of infinite.  GELU and SiLU are within a few units of 2^-24 of |z|. */
 FK_API fk_status fk_linear(const void *X, fk_dtype dtype, int64_t N, int d, const void *W,
                            int m, const float *bias, fk_activation act, const void *residual,
                            void *Y, void *Z, void *ws, size_t ws_bytes, fk_stream_t stream);
@@ -459,7 +465,8 @@ FK_API fk_status fk_linear(const void *X, fk_dtype dtype, int64_t N, int d, cons
 /* Gradients of fk_linear: with G = dY act'(Z) (Z the pre-activation it returned; NULL with
  * FK_ACT_NONE; relu'(0) = 0),
  *   dX = G W (N x d), dW = G^T X (m x d), dbias = sum_i G (m floats), each optional.
- * The residual's gradient is dY itself. */
+ * The residual's gradient is dY itself.  With FK_BF16 and an activation, G is rounded to bf16
+ * as the operand of the two products (dbias takes it before that). */
 FK_API fk_status fk_linear_backward(const void *dY, const void *X, fk_dtype dtype, int64_t N,
                                     int d, const void *W, int m, fk_activation act,
                                     const void *Z, void *dX, void *dW, float *dbias, void *ws,
@@ -483,7 +490,7 @@ FK_API fk_status fk_balance_workspace_size(int64_t N, int K, fk_dtype dtype, siz
  *   *loss = coef K sum_k f_k (sum_i p_ik / n)         (1 for an even selection, coef 1)
  *   dS_ij = coef scale (K / n) p_ij (f_j - sum_k f_k p_ik)     (N x K, optional, may be S)
  * Padding rows' scores are not used and their gradients are 0; a score of -inf has p = 0, and
- * so has every score of a row of -inf.  counts and rows (device) come from
+ * so has every score of a row of -inf.  0 < scale <= 1e37.  counts and rows (device) come from
  * fk_balance_counts; labels only tell which rows are padding.  With counts and rows of all
  * shards, the shards' losses add up to the whole. */
 FK_API fk_status fk_balance_loss(const void *S, fk_dtype dtype, int64_t N, int K,

@@ -667,6 +667,87 @@ def test_unaligned_views_give_the_aligned_bits(fk, d, m, dtype):
                      * (c.abs() + c.abs().max())).all()), i
 
 
+def test_calls_on_two_streams_at_once(fk):
+    """Two chains of calls that overlap on the GPU, each with a workspace of its own."""
+    chains = [head_setup(fk, 3000, 256, 512, 64, seed=s) for s in (0, 50)]
+    for p, b, ws in chains:
+        head_pass(fk, p, b, ws)
+    torch.cuda.synchronize()
+    first = [{k: v.clone() for k, v in b.items() if k != "aws"} for _, b, _ in chains]
+    streams = [torch.cuda.Stream() for _ in chains]
+    for _ in range(5):
+        for (p, b, ws), s in zip(chains, streams):
+            head_pass(fk, p, b, ws, s)
+    torch.cuda.synchronize()
+    for (_, b, _), want in zip(chains, first):
+        for k, v in want.items():
+            assert torch.equal(b[k], v), k
+
+
+def test_the_first_call_of_a_process_can_be_captured(cuda_device):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = (
+        "import sys, torch\n"
+        f"sys.path[:0] = [{root!r}, {os.path.join(root, 'tests')!r}]\n"
+        "from exact_lloyd_means_b200 import fk\n"
+        "t = torch.float32\n"
+        "X, W = torch.randn(300, 72, device='cuda'), torch.randn(40, 72, device='cuda')\n"
+        "Y, Z = torch.empty(300, 40, device='cuda'), torch.empty(300, 40, device='cuda')\n"
+        "n, m, r = torch.empty_like(X), torch.empty(300, device='cuda'), torch.empty(300, "
+        "device='cuda')\n"
+        "dX, dW = torch.empty_like(X), torch.empty_like(W)\n"
+        "ws, wb = fk.linear_workspace(300, 72, 40), fk.linear_backward_workspace(300, 72, 40)\n"
+        "lab = torch.arange(300, device='cuda', dtype=torch.int32) % 40\n"
+        "c, q = (torch.empty(k, device='cuda', dtype=torch.int32) for k in (40, 1))\n"
+        "L, bw = torch.empty(1, device='cuda'), fk.balance_workspace(300, 40)\n"
+        "def run():\n"
+        "    fk.fk_layer_norm(X, None, None, n, 1e-5, m, r)\n"
+        "    fk.fk_linear(n, W, Y, ws, act='gelu', Z=Z)\n"
+        "    fk.fk_balance_counts(lab, c, q)\n"
+        "    fk.fk_balance_loss(Y, lab, c, q, L, Y, bw)\n"
+        "    fk.fk_linear_backward(Y, n, W, wb, act='gelu', Z=Z, dX=dX, dW=dW)\n"
+        "torch.cuda.synchronize()\n"
+        "g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g):\n"
+        "    run()\n"
+        "g.replay(); torch.cuda.synchronize()\n"
+        "a = [v.clone() for v in (Y, dX, dW, L)]\n"
+        "run(); torch.cuda.synchronize()\n"
+        "print(all(torch.equal(x, y) for x, y in zip(a, (Y, dX, dW, L))), "
+        "bool(dW.isfinite().all()))\n")
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stderr
+    assert out.stdout.split() == ["True", "True"]
+
+
+def test_binding_refuses_tensors_it_would_misread(fk):
+    X, W, Y = rnd((12, 8)), rnd((4, 8)), torch.empty((12, 4), device="cuda")
+    ws = fk.linear_workspace(12, 8, 4)
+    for bad in (dict(X=rnd((8, 12)).t()), dict(W=rnd((8, 4)).t()), dict(Y=Y.t().contiguous().t()),
+                dict(W=rnd((4, 9))), dict(bias=rnd((5,))), dict(Y=torch.empty(12, 4)),
+                dict(residual=rnd((12, 5))), dict(X=rnd((12, 8, 1)))):
+        a = dict(dict(X=X, W=W, Y=Y, ws=ws), **bad)
+        with pytest.raises(ValueError):
+            fk.fk_linear(**a)
+    for bad in (dict(W=W.bfloat16()), dict(Y=Y.bfloat16()), dict(bias=rnd((4,)).double()),
+                dict(X=X.half(), W=W.half(), Y=Y.half()), dict(ws=ws.int())):
+        a = dict(dict(X=X, W=W, Y=Y, ws=ws), **bad)
+        with pytest.raises(TypeError):
+            fk.fk_linear(**a)
+    with pytest.raises(ValueError):
+        fk.fk_linear(X, W, Y, ws, act="tanh")
+    with pytest.raises(fk.FkError) as e:
+        fk.fk_linear(X, W, Y, ws[:64])
+    assert e.value.status == fk.FK_ERR_WORKSPACE
+    with pytest.raises(fk.FkError) as e:  # an output over an input
+        fk.fk_layer_norm_backward(X, X, None, rnd((12,)), rnd((12,)), X, None, None,
+                                  fk.layer_norm_backward_workspace(12, 8))
+    assert e.value.status == fk.FK_ERR_INVALID_ARG
+
+
 def test_no_rows(fk):
     X = torch.empty((0, 24), device="cuda")
     W, v = rnd((8, 24)), rnd((24,))

@@ -126,7 +126,8 @@ def test_balance_refusals(fk):
     nan, inf = float("nan"), float("inf")
     for bad in (dict(N=-1), dict(K=0), dict(top=0), dict(S=None), dict(labels=None),
                 dict(counts=None), dict(rows=None), dict(loss=None), dict(scale=0.0),
-                dict(scale=-1.0), dict(scale=nan), dict(scale=inf), dict(coef=nan),
+                dict(scale=-1.0), dict(scale=nan), dict(scale=inf), dict(scale=1e38),
+                dict(coef=nan),
                 dict(coef=inf), dict(dS=_at(0) + 4), dict(dS=_at(1)), dict(loss=_at(3)),
                 dict(ws=_at(0)), dict(N=1 << 30, top=2)):
         assert loss(**bad) == fk.FK_ERR_INVALID_ARG, bad
