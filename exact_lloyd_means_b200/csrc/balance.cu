@@ -162,10 +162,10 @@ template <int W>
 __device__ __forceinline__ float lanes_max(float m) {
     if constexpr (W == 32) {
         asm("redux.sync.max.NaN.f32 %0, %0, 0xffffffff;" : "+f"(m));
-        return m;
-    }
+    } else {
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = W / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
     return m;
 }
 // Both sums in one chain: even lanes go on with z, odd lanes with t.

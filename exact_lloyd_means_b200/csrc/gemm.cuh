@@ -37,11 +37,16 @@ struct GemmArgs {
     uint32_t *err;
 };
 
-GemmPlan gemm_plan(int64_t rows, int64_t cols, int64_t depth, fk_dtype dtype);
+// Up to two products of the same type run in one launch, with tiles of one shape.
+constexpr int kMaxProducts = 2;
+struct GemmSize {
+    int64_t rows, cols, depth;
+};
+void gemm_plan(const GemmSize *sizes, int n, fk_dtype dtype, GemmPlan *plans);
 inline size_t gemm_part_bytes(const GemmPlan &p) {
     return p.splits > 1 ? sizeof(float) * p.tail * p.splits * p.tile() : 0;
 }
-cudaError_t launch_gemm(const GemmArgs &a, const GemmPlan &p, cudaStream_t st);
+cudaError_t launch_gemm(const GemmArgs *args, const GemmPlan *plans, int n, cudaStream_t st);
 
 // ----------------------------------------------------------------- epilogue
 // One branch for all the values, which keeps their chains of dependent instructions side by

@@ -20,6 +20,8 @@
 //     own and the five small products into another, so that these are not rounded to the
 //     size of the sum, and the sum is rounded no more often than that of bf16 operands;
 //   * every wait is bounded; on expiry the CTA records the timeout and winds down.
+#include <type_traits>
+
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -34,8 +36,6 @@ namespace {
 
 constexpr int kBandRows = 8;  // tiles of one column band that run side by side
 
-// OV = consecutive columns an epilogue thread writes at once: 32 or 16 bytes of them, or one
-// column, where rows of the outputs do not start on such boundaries.
 // The tensor cores cut what they add to an accumulator (about 2^-24 of the sum a step of 16,
 // always towards zero: 4.4e-6 of the result at a depth of 4096).  So fp32 products are
 // accumulated in runs of 256 of the depth, 2e-7 each, and the runs added to fp32 registers;
@@ -43,6 +43,8 @@ constexpr int kBandRows = 8;  // tiles of one column band that run side by side
 constexpr int kRunChunks = 4;
 constexpr int kMaxBf16Chunks = 2048;
 
+// OV = consecutive columns an epilogue thread writes at once: 32 or 16 bytes of them, or one
+// column, where rows of the outputs do not start on such boundaries.
 template <int CG, int BN, int NP, int OV>
 struct GemmCfg {
     static constexpr int kABytes = kBM * kBK * 2;  // one plane
@@ -75,8 +77,18 @@ struct GemmShape {
     int nkc;      // chunks of 64 in the depth
     int splits;
     int a_mn, b_mn;
-    int64_t tiles_r, tiles_c, units;
+    int64_t tiles_r, tiles_c;
     int64_t full, tail;  // tiles with the whole depth, tiles with their depth cut
+};
+
+// The products of a launch: the units of the first, then those of the second.
+struct alignas(64) GemmJobs {
+    CUtensorMap a[kMaxProducts], b[kMaxProducts];
+    GemmShape shape[kMaxProducts];
+    Epilogue ep[kMaxProducts];
+    float *part[kMaxProducts];
+    int bvec[kMaxProducts];  // the bias in 16-byte vectors
+    int64_t second, units;   // first unit of the second product, all units
 };
 
 // Tile t in the order of work: bands of kBandRows row tiles, rows fastest within a band, so that
@@ -91,29 +103,43 @@ __host__ __device__ __forceinline__ void tile_of(const GemmShape &s, int64_t t, 
     tr = band * kBandRows + (in - tc * h);
 }
 
-// Unit u: its tile, its chunks of the depth and, where they are not all, its partial product.
+// Unit u: its chunks of the depth, which part of it they are (0 of 1 for a whole one) ...
+struct Chunks {
+    int k0, k1, split;
+};
+__device__ __forceinline__ Chunks chunks_of(const GemmShape &s, int64_t u) {
+    if (u < s.full || s.splits == 1) return Chunks{0, s.nkc, 0};
+    const int split = static_cast<int>((u - s.full) / s.tail);
+    return Chunks{static_cast<int>(static_cast<int64_t>(s.nkc) * split / s.splits),
+                  static_cast<int>(static_cast<int64_t>(s.nkc) * (split + 1) / s.splits), split};
+}
+// ... its tile and, where its chunks are not all, its partial product.
 struct Unit {
     int64_t tr, tc, part;
     int k0, k1;
 };
 __device__ __forceinline__ Unit unit_of(const GemmShape &s, int64_t u) {
     Unit r;
-    int64_t t = u;
+    const Chunks c = chunks_of(s, u);
+    r.k0 = c.k0;
+    r.k1 = c.k1;
     r.part = -1;
-    r.k0 = 0;
-    r.k1 = s.nkc;
-    if (u >= s.full) {
-        const int64_t v = u - s.full;
-        const int split = static_cast<int>(v / s.tail);
-        t = s.full + (v - split * s.tail);
-        if (s.splits > 1) {
-            r.part = (v - split * s.tail) * s.splits + split;
-            r.k0 = static_cast<int>(static_cast<int64_t>(s.nkc) * split / s.splits);
-            r.k1 = static_cast<int>(static_cast<int64_t>(s.nkc) * (split + 1) / s.splits);
-        }
+    if (u >= s.full && s.splits > 1) {
+        u -= c.split * s.tail;
+        r.part = (u - s.full) * s.splits + c.split;
     }
-    tile_of(s, t, r.tr, r.tc);
+    tile_of(s, u, r.tr, r.tc);
     return r;
+}
+
+// f with the operands' majors as constants: the loops over the depth are the kernel's pulse,
+// and deciding in them how to load cost a 65,536 x 768 x 4096 product 6%.  (An MN-major A
+// comes with an MN-major B: dW.)
+template <typename F>
+__device__ __forceinline__ bool by_major(bool a_mn, bool b_mn, F &&f) {
+    if (a_mn) return f(std::true_type{}, std::true_type{});
+    if (b_mn) return f(std::false_type{}, std::true_type{});
+    return f(std::false_type{}, std::false_type{});
 }
 
 __device__ __forceinline__ void gemm_timeout(volatile uint32_t *abort_flag, uint32_t *err) {
@@ -123,9 +149,8 @@ __device__ __forceinline__ void gemm_timeout(volatile uint32_t *abort_flag, uint
 
 template <int CG, int BN, typename T, int OV>
 __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
-    gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                const GemmShape sh, const Epilogue ep, int bvec, float *__restrict__ part,
-                uint32_t *__restrict__ err, uint64_t wait_ns) {
+    gemm_kernel(const __grid_constant__ GemmJobs jobs, uint32_t *__restrict__ err,
+                uint64_t wait_ns) {
     constexpr int NP = kPlanes<T>;
     using Cfg = GemmCfg<CG, BN, NP, OV>;
     constexpr int S = Cfg::kStages;
@@ -159,8 +184,8 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
         ptx::mbar_init(drain, 1);
         *abort_flag = 0u;
         ptx::fence_mbar_init();
-        ptx::prefetch_tmap(&tmA);
-        ptx::prefetch_tmap(&tmB);
+        ptx::prefetch_tmap(&jobs.a[0]);
+        ptx::prefetch_tmap(&jobs.b[0]);
     }
     if (warp == 1) {
         if constexpr (CG == 2) {
@@ -186,122 +211,141 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
                 CG == 2 ? ptx::mapa_shared(ptx::smem_u32(full), 0) : 0u;
             uint32_t stage = 0, phase = 0;
             bool ok = true;
-            for (int64_t u = first; u < sh.units && ok; u += step) {
-                const Unit un = unit_of(sh, u);
+            for (int64_t u = first; u < jobs.units && ok; u += step) {
+                const bool j = u >= jobs.second;
+                const Unit un = j ? unit_of(jobs.shape[1], u - jobs.second)
+                                  : unit_of(jobs.shape[0], u);
+                const CUtensorMap *ma = j ? &jobs.a[1] : &jobs.a[0];
+                const CUtensorMap *mb = j ? &jobs.b[1] : &jobs.b[0];
                 const int r0 = static_cast<int>(un.tr * (kBM * CG) + rank * kBM);
                 const int c0 = static_cast<int>(un.tc * BN + rank * Cfg::kBRows);
-                for (int kc = un.k0; kc < un.k1; ++kc) {
-                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag, wait_ns)) {
-                        gemm_timeout(abort_flag, err);
-                        ok = false;
-                        break;
-                    }
-                    if (rank == 0)
-                        ptx::mbar_arrive_expect_tx(&full[stage], CG * Cfg::kStageBytes);
-                    const int k = kc * kBK;
-                    auto load = [&](uint8_t *dst, const CUtensorMap *map, int x, int y, int p) {
-                        if constexpr (CG == 2)
-                            ptx::tma_load_3d_pair(dst, map, full_c + stage * 8, x, y, p);
-                        else
-                            ptx::tma_load_3d(dst, map, &full[stage], x, y, p);
-                    };
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        uint8_t *sa = smem + stage * Cfg::kStageBytes + p * Cfg::kABytes;
-                        uint8_t *sb = smem + stage * Cfg::kStageBytes + NP * Cfg::kABytes +
-                                      p * Cfg::kBBytes;
-                        if (sh.a_mn) {
-#pragma unroll
-                            for (int b = 0; b < kBM / 64; ++b)
-                                load(sa + b * 8192, &tmA, r0 + b * 64, k, p);
-                        } else {
-                            load(sa, &tmA, k, r0, p);
-                        }
-                        if (sh.b_mn) {
-#pragma unroll
-                            for (int b = 0; b < Cfg::kBRows / 64; ++b)
-                                load(sb + b * 8192, &tmB, c0 + b * 64, k, p);
-                        } else {
-                            load(sb, &tmB, k, c0, p);
-                        }
-                    }
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-            }
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0 && rank == 0) {
-            const uint32_t idesc = ptx::idesc_bf16_f32(kBM * CG, BN) |
-                                   ptx::idesc_mn_major(sh.a_mn != 0, sh.b_mn != 0);
-            const uint64_t ka = sh.a_mn ? 2048 / 16 : 2, kb = sh.b_mn ? 2048 / 16 : 2;
-            // chunks of one accumulation
-            constexpr int kRun = NP == 3 ? kRunChunks : 0x40000000;
-            uint32_t stage = 0, phase = 0, it = 0;
-            bool ok = true;
-            for (int64_t u = first; u < sh.units && ok; u += step) {
-                const Unit un = unit_of(sh, u);
-                for (int k0 = un.k0; k0 < un.k1 && ok; k0 += kRun, ++it) {
-                    const uint32_t acc = it & 1u;
-                    if (!ptx::mbar_wait(&tempty[acc], ((it >> 1) & 1u) ^ 1u, abort_flag, wait_ns)) {
-                        gemm_timeout(abort_flag, err);
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
-                    const uint32_t dt = tmem + acc * Cfg::kAccCols;
-                    const int n = un.k1 - k0 < kRun ? un.k1 - k0 : kRun;
-                    for (int i = 0; i < n; ++i) {
-                        if (!ptx::mbar_wait(&full[stage], phase, abort_flag, wait_ns)) {
+                ok = by_major((j ? jobs.shape[1].a_mn : jobs.shape[0].a_mn) != 0,
+                              (j ? jobs.shape[1].b_mn : jobs.shape[0].b_mn) != 0,
+                              [&](auto a_mn, auto b_mn) {
+                    for (int kc = un.k0; kc < un.k1; ++kc) {
+                        if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, abort_flag, wait_ns)) {
                             gemm_timeout(abort_flag, err);
-                            ok = false;
-                            break;
+                            return false;
                         }
-                        ptx::tc_fence_after();
-                        const uint32_t sa = ptx::smem_u32(smem + stage * Cfg::kStageBytes);
-                        const uint32_t sb = sa + NP * Cfg::kABytes;
-                        const uint64_t da = sh.a_mn ? ptx::sdesc_mn_sw128(sa)
-                                                    : ptx::sdesc_k_sw128(sa);
-                        const uint64_t db = sh.b_mn ? ptx::sdesc_mn_sw128(sb)
-                                                    : ptx::sdesc_k_sw128(sb);
-                        auto mma = [&](uint32_t d, int pa, int pb, int ks, uint32_t more) {
-                            const uint64_t x = da + pa * (Cfg::kABytes / 16) + ks * ka;
-                            const uint64_t y = db + pb * (Cfg::kBBytes / 16) + ks * kb;
+                        if (rank == 0)
+                            ptx::mbar_arrive_expect_tx(&full[stage], CG * Cfg::kStageBytes);
+                        const int k = kc * kBK;
+                        auto load = [&](uint8_t *dst, const CUtensorMap *map, int x, int y,
+                                        int p) {
                             if constexpr (CG == 2)
-                                ptx::mma_bf16_ss_pair(d, x, y, idesc, more);
+                                ptx::tma_load_3d_pair(dst, map, full_c + stage * 8, x, y, p);
                             else
-                                ptx::mma_bf16_ss(d, x, y, idesc, more);
+                                ptx::tma_load_3d(dst, map, &full[stage], x, y, p);
                         };
 #pragma unroll
-                        for (int ks = 0; ks < kBK / 16; ++ks) {
-                            const uint32_t more = i > 0 || ks > 0 ? 1u : 0u;
-                            mma(dt, 0, 0, ks, more);
-                            if constexpr (NP == 3) {
-                                mma(dt + BN, 0, 2, ks, more);
-                                mma(dt + BN, 1, 1, ks, 1u);
-                                mma(dt + BN, 2, 0, ks, 1u);
-                                mma(dt + BN, 0, 1, ks, 1u);
-                                mma(dt + BN, 1, 0, ks, 1u);
+                        for (int p = 0; p < NP; ++p) {
+                            uint8_t *sa = smem + stage * Cfg::kStageBytes + p * Cfg::kABytes;
+                            uint8_t *sb = smem + stage * Cfg::kStageBytes + NP * Cfg::kABytes +
+                                          p * Cfg::kBBytes;
+                            if constexpr (decltype(a_mn)::value) {
+#pragma unroll
+                                for (int b = 0; b < kBM / 64; ++b)
+                                    load(sa + b * 8192, ma, r0 + b * 64, k, p);
+                            } else {
+                                load(sa, ma, k, r0, p);
+                            }
+                            if constexpr (decltype(b_mn)::value) {
+#pragma unroll
+                                for (int b = 0; b < Cfg::kBRows / 64; ++b)
+                                    load(sb + b * 8192, mb, c0 + b * 64, k, p);
+                            } else {
+                                load(sb, mb, k, c0, p);
                             }
                         }
-                        if constexpr (CG == 2)
-                            ptx::mma_commit_pair(&empty[stage], 0x3);
-                        else
-                            ptx::mma_commit(&empty[stage]);
                         if (++stage == S) {
                             stage = 0;
                             phase ^= 1u;
                         }
                     }
-                    if (!ok) break;
-                    if constexpr (CG == 2)
-                        ptx::mma_commit_pair(&tfull[acc], 0x3);
-                    else
-                        ptx::mma_commit(&tfull[acc]);
-                }
+                    return true;
+                });
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0 && rank == 0) {
+            // chunks of one accumulation
+            constexpr int kRun = NP == 3 ? kRunChunks : 0x40000000;
+            uint32_t stage = 0, phase = 0, it = 0;
+            bool ok = true;
+            for (int64_t u = first; u < jobs.units && ok; u += step) {
+                const bool j = u >= jobs.second;
+                // (no more than it needs: what this thread does between tiles leaves the
+                // tensor cores idle)
+                const Chunks un = j ? chunks_of(jobs.shape[1], u - jobs.second)
+                                    : chunks_of(jobs.shape[0], u);
+                ok = by_major((j ? jobs.shape[1].a_mn : jobs.shape[0].a_mn) != 0,
+                              (j ? jobs.shape[1].b_mn : jobs.shape[0].b_mn) != 0,
+                              [&](auto a_mn, auto b_mn) {
+                    constexpr bool AM = decltype(a_mn)::value, BM = decltype(b_mn)::value;
+                    constexpr uint32_t idesc =
+                        ptx::idesc_bf16_f32(kBM * CG, BN) | ptx::idesc_mn_major(AM, BM);
+                    const uint32_t sa = ptx::smem_u32(smem);
+                    const uint32_t sb = sa + NP * Cfg::kABytes;
+                    const uint64_t da0 = AM ? ptx::sdesc_mn_sw128(sa) : ptx::sdesc_k_sw128(sa);
+                    const uint64_t db0 = BM ? ptx::sdesc_mn_sw128(sb) : ptx::sdesc_k_sw128(sb);
+                    for (int k0 = un.k0; k0 < un.k1; k0 += kRun, ++it) {
+                        const uint32_t acc = it & 1u;
+                        if (!ptx::mbar_wait(&tempty[acc], ((it >> 1) & 1u) ^ 1u, abort_flag,
+                                            wait_ns)) {
+                            gemm_timeout(abort_flag, err);
+                            return false;
+                        }
+                        ptx::tc_fence_after();
+                        const uint32_t dt = tmem + acc * Cfg::kAccCols;
+                        const int n = un.k1 - k0 < kRun ? un.k1 - k0 : kRun;
+                        for (int i = 0; i < n; ++i) {
+                            if (!ptx::mbar_wait(&full[stage], phase, abort_flag, wait_ns)) {
+                                gemm_timeout(abort_flag, err);
+                                return false;
+                            }
+                            ptx::tc_fence_after();
+                            // (an address field counts 16 bytes)
+                            const uint64_t da = da0 + stage * (Cfg::kStageBytes / 16);
+                            const uint64_t db = db0 + stage * (Cfg::kStageBytes / 16);
+                            auto mma = [&](uint32_t d, int pa, int pb, int ks, uint32_t more) {
+                                const uint64_t x =
+                                    da + pa * (Cfg::kABytes / 16) + ks * (AM ? 128 : 2);
+                                const uint64_t y =
+                                    db + pb * (Cfg::kBBytes / 16) + ks * (BM ? 128 : 2);
+                                if constexpr (CG == 2)
+                                    ptx::mma_bf16_ss_pair(d, x, y, idesc, more);
+                                else
+                                    ptx::mma_bf16_ss(d, x, y, idesc, more);
+                            };
+#pragma unroll
+                            for (int ks = 0; ks < kBK / 16; ++ks) {
+                                const uint32_t more = i > 0 || ks > 0 ? 1u : 0u;
+                                mma(dt, 0, 0, ks, more);
+                                if constexpr (NP == 3) {
+                                    mma(dt + BN, 0, 2, ks, more);
+                                    mma(dt + BN, 1, 1, ks, 1u);
+                                    mma(dt + BN, 2, 0, ks, 1u);
+                                    mma(dt + BN, 0, 1, ks, 1u);
+                                    mma(dt + BN, 1, 0, ks, 1u);
+                                }
+                            }
+                            if constexpr (CG == 2)
+                                ptx::mma_commit_pair(&empty[stage], 0x3);
+                            else
+                                ptx::mma_commit(&empty[stage]);
+                            if (++stage == S) {
+                                stage = 0;
+                                phase ^= 1u;
+                            }
+                        }
+                        if constexpr (CG == 2)
+                            ptx::mma_commit_pair(&tfull[acc], 0x3);
+                        else
+                            ptx::mma_commit(&tfull[acc]);
+                    }
+                    return true;
+                });
             }
             if (!ok) {
                 if constexpr (CG == 2)
@@ -323,8 +367,16 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
         constexpr int C = Cfg::kGroupCols / 32;
         uint32_t it = 0;
         bool ok = true;
-        for (int64_t u = first; u < sh.units && ok; u += step) {
-            const Unit un = unit_of(sh, u);
+        for (int64_t u = first; u < jobs.units && ok; u += step) {
+            // (by value and by fixed index: a reference picked here is read from memory again
+            // at every use)
+            const bool j = u >= jobs.second;
+            const Epilogue ep = j ? jobs.ep[1] : jobs.ep[0];
+            const int64_t rows = j ? jobs.shape[1].rows : jobs.shape[0].rows;
+            const int bvec = j ? jobs.bvec[1] : jobs.bvec[0];
+            float *part = j ? jobs.part[1] : jobs.part[0];
+            const Unit un = j ? unit_of(jobs.shape[1], u - jobs.second)
+                              : unit_of(jobs.shape[0], u);
             const int64_t r0 = un.tr * (kBM * CG) + rank * kBM + q * 32;
             const int64_t c0 = un.tc * BN + g * Cfg::kGroupCols;
             // columns c0 + 32 c .. + 31 of this thread's row, finished
@@ -343,9 +395,9 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
                     float z[32 / OV][OV];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) z[j / OV][j % OV] = v[j];
-                    Pieces o{(r0 + lane) * sh.cols + col, OV, col, OV, 0u};
-                    const int64_t left = (sh.cols - col) / OV;  // pieces before the last column
-                    if (r0 + lane >= sh.rows || left <= 0) return;
+                    Pieces o{(r0 + lane) * ep.cols + col, OV, col, OV, 0u};
+                    const int64_t left = (ep.cols - col) / OV;  // pieces before the last column
+                    if (r0 + lane >= rows || left <= 0) return;
                     if (left >= 32 / OV) {
                         epilogue_pieces<T, OV, true>(ep, o, bvec, z);
                     } else {
@@ -361,10 +413,10 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
                         float z[8][1];
 #pragma unroll
                         for (int p = 0; p < 8; ++p) z[p][0] = st[(rr + p) * 33 + lane];
-                        const int64_t left = sh.rows - (r0 + rr);
+                        const int64_t left = rows - (r0 + rr);
                         const uint32_t n = left <= 0 ? 0u : (left < 8 ? (1u << left) - 1u : 0xffu);
-                        const Pieces o{(r0 + rr) * sh.cols + col + lane, sh.cols, col + lane, 0,
-                                       col + lane < sh.cols ? n : 0u};
+                        const Pieces o{(r0 + rr) * ep.cols + col + lane, ep.cols, col + lane, 0,
+                                       col + lane < ep.cols ? n : 0u};
                         epilogue_pieces<T, 1, false>(ep, o, 0, z);
                     }
                     __syncwarp();
@@ -460,17 +512,19 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
 }
 
 // Join the partial products of the tail tiles, in order, and apply the epilogue.  Block (x,
-// y): rows of tail tile x.
+// y): rows of tail tile x, those of the first product (`split0` of them) before the second's.
 template <typename T, int V>
 __global__ void __launch_bounds__(256)
-    gemm_join_kernel(const float *__restrict__ part, const GemmShape s, int tile_rows, int bn,
-                     const Epilogue ep, int bvec) {
+    gemm_join_kernel(const __grid_constant__ GemmJobs jobs, int split0, int tile_rows, int bn) {
     pdl_wait();
     pdl_trigger();
+    const int job = static_cast<int>(blockIdx.x) >= split0;
+    const int64_t tile = static_cast<int64_t>(blockIdx.x) - (job ? split0 : 0);
+    const GemmShape &s = jobs.shape[job];
     int64_t tr, tc;
-    tile_of(s, s.full + blockIdx.x, tr, tc);
+    tile_of(s, s.full + tile, tr, tc);
     const int64_t size = static_cast<int64_t>(tile_rows) * bn;
-    const float *base = part + static_cast<int64_t>(blockIdx.x) * s.splits * size;
+    const float *base = jobs.part[job] + tile * s.splits * size;
     const int per_row = bn / V;
     for (int t = blockIdx.y * 256 + threadIdx.x; t < tile_rows * per_row; t += gridDim.y * 256) {
         const int lr = t / per_row, lc = (t - lr * per_row) * V;
@@ -488,7 +542,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int j = 0; j < V; ++j) z[0][j] += f[j];
         }
-        epilogue_pieces<T, V, true>(ep, o, bvec, z);
+        epilogue_pieces<T, V, true>(jobs.ep[job], o, jobs.bvec[job], z);
     }
 }
 
@@ -510,42 +564,50 @@ bool operand_map(CUtensorMap *m, const GemmOperand &o, int64_t outer, int64_t in
 }
 
 template <int CG, int BN, typename T, int OV>
-cudaError_t launch_cfg(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
+cudaError_t launch_cfg(const GemmArgs *args, const GemmPlan *plans, int n, cudaStream_t st) {
     using Cfg = GemmCfg<CG, BN, kPlanes<T>, OV>;
     auto kernel = gemm_kernel<CG, BN, T, OV>;
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t e = smem_opt_in(kernel, Cfg::kSmemBytes, smem_set);
     if (e != cudaSuccess) return e;
-    CUtensorMap tA, tB;
-    const bool ok =
-        (a.A.mn_major ? operand_map(&tA, a.A, a.depth, a.rows, kPlanes<T>, 64)
-                      : operand_map(&tA, a.A, a.rows, a.depth, kPlanes<T>, kBM)) &&
-        (a.B.mn_major ? operand_map(&tB, a.B, a.depth, a.cols, kPlanes<T>, 64)
-                      : operand_map(&tB, a.B, a.cols, a.depth, kPlanes<T>, Cfg::kBRows));
-    if (!ok) return cudaErrorInvalidValue;
-    GemmShape s{};
-    s.rows = a.rows;
-    s.cols = a.cols;
-    s.nkc = static_cast<int>(ceil_div(a.depth, kBK));
-    s.splits = p.splits;
-    s.a_mn = a.A.mn_major;
-    s.b_mn = a.B.mn_major;
-    s.tiles_r = ceil_div(a.rows, kBM * CG);
-    s.tiles_c = ceil_div(a.cols, BN);
-    s.full = p.full;
-    s.tail = p.tail;
-    s.units = p.full + p.tail * p.splits;
-    const int bvec = aligned(a.bias, 16);
-    Epilogue ep{};
-    ep.bias = a.bias;
-    ep.R = a.R;
-    ep.C = a.C;
-    ep.Z = a.Z;
-    ep.cols = a.cols;
-    ep.act = a.act;
+    GemmJobs jobs{};
+    int64_t joined[kMaxProducts] = {};  // tail tiles to join
+    for (int i = 0; i < n; ++i) {
+        const GemmArgs &a = args[i];
+        const GemmPlan &p = plans[i];
+        const bool ok =
+            (a.A.mn_major ? operand_map(&jobs.a[i], a.A, a.depth, a.rows, kPlanes<T>, 64)
+                          : operand_map(&jobs.a[i], a.A, a.rows, a.depth, kPlanes<T>, kBM)) &&
+            (a.B.mn_major ? operand_map(&jobs.b[i], a.B, a.depth, a.cols, kPlanes<T>, 64)
+                          : operand_map(&jobs.b[i], a.B, a.cols, a.depth, kPlanes<T>, Cfg::kBRows));
+        if (!ok) return cudaErrorInvalidValue;
+        GemmShape &s = jobs.shape[i];
+        s.rows = a.rows;
+        s.cols = a.cols;
+        s.nkc = static_cast<int>(ceil_div(a.depth, kBK));
+        s.splits = p.splits;
+        s.a_mn = a.A.mn_major;
+        s.b_mn = a.B.mn_major;
+        s.tiles_r = ceil_div(a.rows, kBM * CG);
+        s.tiles_c = ceil_div(a.cols, BN);
+        s.full = p.full;
+        s.tail = p.tail;
+        jobs.bvec[i] = aligned(a.bias, 16);
+        jobs.part[i] = a.part;
+        Epilogue &ep = jobs.ep[i];
+        ep.bias = a.bias;
+        ep.R = a.R;
+        ep.C = a.C;
+        ep.Z = a.Z;
+        ep.cols = a.cols;
+        ep.act = a.act;
+        jobs.units += p.full + p.tail * p.splits;
+        if (i == 0) jobs.second = jobs.units;
+        joined[i] = p.splits > 1 ? p.tail : 0;
+    }
     const int64_t slots = device_sm_count() / CG;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(CG * (s.units < slots ? s.units : slots)));
+    cfg.gridDim = dim3(static_cast<unsigned>(CG * (jobs.units < slots ? jobs.units : slots)));
     cfg.blockDim = dim3(Cfg::kThreads);
     cfg.dynamicSmemBytes = Cfg::kSmemBytes;
     cfg.stream = st;
@@ -558,41 +620,45 @@ cudaError_t launch_cfg(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 2 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, tA, tB, s, ep, bvec, a.part, a.err, kDefaultWaitNs);
+    e = cudaLaunchKernelEx(&cfg, kernel, jobs, args[0].err, kDefaultWaitNs);
     if (e != cudaSuccess) return e;
     note_launch();
-    if (p.splits > 1) {
+    const int64_t tiles = joined[0] + joined[1];
+    if (tiles > 0) {
         constexpr int JV = OV > kVec<T> ? kVec<T> : OV;  // 16 bytes of output a thread
-        const int64_t want = ceil_div(static_cast<int64_t>(device_sm_count()) * 8, p.tail);
-        const int64_t most = p.tile() / JV / 256;
+        const int64_t want = ceil_div(static_cast<int64_t>(device_sm_count()) * 8, tiles);
+        const int64_t most = int64_t(kBM) * CG * BN / JV / 256;
         e = launch_pdl(gemm_join_kernel<T, JV>,
-                       dim3(static_cast<unsigned>(p.tail),
+                       dim3(static_cast<unsigned>(tiles),
                             static_cast<unsigned>(want < most ? want : most)),
-                       dim3(256), 0, st, static_cast<const float *>(a.part), s, kBM * CG, BN, ep,
-                       bvec);
+                       dim3(256), 0, st, jobs, static_cast<int>(joined[0]), kBM * CG, BN);
         if (e == cudaSuccess) note_launch();
     }
     return e;
 }
 
 template <typename T, int OV>
-cudaError_t launch_v(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
+cudaError_t launch_v(const GemmArgs *a, const GemmPlan *p, int n, cudaStream_t st) {
     // (fp32: two accumulators a tile, so half the columns)
-    if (p.cg == 2) return launch_cfg<2, 256 / (kPlanes<T> == 3 ? 2 : 1), T, OV>(a, p, st);
-    if (p.bn == 128) return launch_cfg<1, 128, T, OV>(a, p, st);
-    return launch_cfg<1, 64, T, OV>(a, p, st);
+    if (p->cg == 2) return launch_cfg<2, 256 / (kPlanes<T> == 3 ? 2 : 1), T, OV>(a, p, n, st);
+    if (p->bn == 128) return launch_cfg<1, 128, T, OV>(a, p, n, st);
+    return launch_cfg<1, 64, T, OV>(a, p, n, st);
 }
 
 template <typename T>
-cudaError_t launch_t(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
+cudaError_t launch_t(const GemmArgs *a, const GemmPlan *p, int n, cudaStream_t st) {
     constexpr int V = kVec<T>;
     auto rows_on = [&](int v) {
         const size_t b = v * sizeof(T);
-        return a.cols % v == 0 && aligned(a.C, b) && aligned(a.Z, b) && aligned(a.R, b);
+        bool ok = true;
+        for (int i = 0; i < n; ++i)
+            ok = ok && a[i].cols % v == 0 && aligned(a[i].C, b) && aligned(a[i].Z, b) &&
+                 aligned(a[i].R, b);
+        return ok;
     };
-    if (rows_on(2 * V)) return launch_v<T, 2 * V>(a, p, st);
-    if (rows_on(V)) return launch_v<T, V>(a, p, st);
-    return launch_v<T, 1>(a, p, st);
+    if (rows_on(2 * V)) return launch_v<T, 2 * V>(a, p, n, st);
+    if (rows_on(V)) return launch_v<T, V>(a, p, n, st);
+    return launch_v<T, 1>(a, p, n, st);
 }
 
 }  // namespace
@@ -605,42 +671,61 @@ cudaError_t launch_t(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
 // those of the last, partial wave may have their depth cut so that it is spread over the
 // GPU, in parts of at least four chunks: that costs a launch (about 4000) and the partial
 // products' way through L2 (about 3000 bytes a cycle).
-GemmPlan gemm_plan(int64_t rows, int64_t cols, int64_t depth, fk_dtype dtype) {
-    const int64_t nkc = ceil_div(depth, kBK);
+// Several products share a tile shape: the one with the least cost in all.
+void gemm_plan(const GemmSize *sizes, int n, fk_dtype dtype, GemmPlan *plans) {
     struct Choice {
         int cg, bn, cycles;
     };
     static constexpr Choice kBf16[3] = {{2, 256, 512}, {1, 128, 512}, {1, 64, 384}};
     static constexpr Choice kF32[3] = {{2, 128, 1536}, {1, 128, 1536}, {1, 64, 1152}};
-    GemmPlan best{};
-    if (dtype == FK_BF16 && nkc > kMaxBf16Chunks) {  // every tile's depth in parts
-        const int64_t tiles = ceil_div(rows, 256) * ceil_div(cols, 256);
-        return GemmPlan{2, 256, static_cast<int>(ceil_div(nkc, kMaxBf16Chunks)), 0, tiles};
-    }
-    double best_cost = -1;
+    double best_all = -1;
     for (const Choice &c : dtype == FK_F32 ? kF32 : kBf16) {
-        const int64_t tiles = ceil_div(rows, kBM * c.cg) * ceil_div(cols, c.bn);
-        const int64_t slots = 148 / c.cg;
-        GemmPlan p{c.cg, c.bn, 1, tiles / slots * slots, tiles % slots};
-        for (p.splits = 1; p.splits <= 32; ++p.splits) {
-            if (p.splits > 1 && (p.tail == 0 || nkc / p.splits < 4)) break;
-            const double waves = static_cast<double>(p.full / slots);
-            const double last = static_cast<double>(ceil_div(p.tail * p.splits, slots));
-            double cost = 4000 + (waves + last) * 500 +
-                          (waves * nkc + last * ceil_div(nkc, p.splits)) * c.cycles;
-            if (p.splits > 1)
-                cost += 4000 + 8.0 * static_cast<double>(p.tail * p.splits * p.tile()) / 3000;
-            if (best_cost < 0 || cost < best_cost) {
-                best_cost = cost;
-                best = p;
+        double all = 0;
+        GemmPlan mine[kMaxProducts] = {};
+        for (int i = 0; i < n; ++i) {
+            const int64_t nkc = ceil_div(sizes[i].depth, kBK);
+            const int64_t tiles =
+                ceil_div(sizes[i].rows, kBM * c.cg) * ceil_div(sizes[i].cols, c.bn);
+            const int64_t slots = 148 / c.cg;
+            const auto cost = [&](const GemmPlan &p) {
+                const double waves = static_cast<double>(p.full / slots);
+                const double last = static_cast<double>(ceil_div(p.tail * p.splits, slots));
+                double t = 4000 + (waves + last) * 500 +
+                           (waves * nkc + last * ceil_div(nkc, p.splits)) * c.cycles;
+                if (p.splits > 1)
+                    t += 4000 + 8.0 * static_cast<double>(p.tail * p.splits * p.tile()) / 3000;
+                return t;
+            };
+            GemmPlan p{c.cg, c.bn, 1, tiles / slots * slots, tiles % slots};
+            if (dtype == FK_BF16 && nkc > kMaxBf16Chunks) {  // every tile's depth in parts
+                p.full = 0;
+                p.tail = tiles;
+                p.splits = static_cast<int>(ceil_div(nkc, kMaxBf16Chunks));
+                mine[i] = p;
+                all += cost(p);
+                continue;
             }
+            double best = -1;
+            for (; p.splits <= 32; ++p.splits) {
+                if (p.splits > 1 && (p.tail == 0 || nkc / p.splits < 4)) break;
+                const double t = cost(p);
+                if (best < 0 || t < best) {
+                    best = t;
+                    mine[i] = p;
+                }
+            }
+            all += best;
+        }
+        if (best_all < 0 || all < best_all) {
+            best_all = all;
+            for (int i = 0; i < n; ++i) plans[i] = mine[i];
         }
     }
-    return best;
 }
 
-cudaError_t launch_gemm(const GemmArgs &a, const GemmPlan &p, cudaStream_t st) {
-    return a.dtype == FK_F32 ? launch_t<float>(a, p, st) : launch_t<uint16_t>(a, p, st);
+cudaError_t launch_gemm(const GemmArgs *args, const GemmPlan *plans, int n, cudaStream_t st) {
+    return args[0].dtype == FK_F32 ? launch_t<float>(args, plans, n, st)
+                                   : launch_t<uint16_t>(args, plans, n, st);
 }
 
 }  // namespace fk

@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(256)
 
 // ----------------------------------------------------------------- layouts
 struct LinearLayout {
-    size_t x = 0, w = 0, g = 0, col = 0, part = 0, total = 0;
+    size_t x = 0, w = 0, g = 0, col = 0, part = 0, part2 = 0, total = 0;
+    GemmPlan plan[kMaxProducts] = {};  // forward; or dX and dW
     int64_t ldd = 0, ldm = 0;  // staged row lengths
     int planes = 1;
     bool stage_x = false, stage_m = false;  // X and W; G and dY
@@ -398,17 +399,17 @@ LinearLayout linear_layout(int64_t N, int d, int m, fk_dtype dtype, bool backwar
     const bool few = !backward && N <= kFewRows;
     L.x = take(L.stage_x && !few ? 2 * L.planes * N * L.ldd : 0);
     L.w = take(L.stage_x && !few ? 2 * L.planes * m * L.ldd : 0);
-    size_t part = 0;
     if (backward) {
         L.g = take(2 * L.planes * N * L.ldm);
         L.col = take(sizeof(float) * static_cast<int64_t>(stage_parts(N, m)) * m);
-        part = gemm_part_bytes(gemm_plan(N, d, m, dtype));
-        const size_t q = gemm_part_bytes(gemm_plan(m, d, N, dtype));
-        part = part > q ? part : q;
+        const GemmSize sizes[2] = {{N, d, m}, {m, d, N}};
+        if (N > 0) gemm_plan(sizes, 2, dtype, L.plan);
     } else if (!few) {
-        part = gemm_part_bytes(gemm_plan(N, m, d, dtype));
+        const GemmSize size{N, m, d};
+        gemm_plan(&size, 1, dtype, L.plan);
     }
-    L.part = take(static_cast<int64_t>(part));
+    L.part = take(static_cast<int64_t>(gemm_part_bytes(L.plan[0])));
+    L.part2 = take(static_cast<int64_t>(gemm_part_bytes(L.plan[1])));
     L.total = o;
     return L;
 }
@@ -428,25 +429,32 @@ GemmOperand operand(StageJobs &jobs, const void *src, int64_t rows, int cols, bo
     return GemmOperand{space, s.ld, mn_major};
 }
 
-// One product: on the tensor cores, or (bf16 operands off 16-byte boundaries) without them.
-cudaError_t product(const GemmArgs &a, cudaStream_t st) {
-    if (aligned(a.A.base, 16) && aligned(a.B.base, 16))
-        return launch_gemm(a, gemm_plan(a.rows, a.cols, a.depth, a.dtype), st);
-    Epilogue ep{};
-    ep.bias = a.bias;
-    ep.R = a.R;
-    ep.C = a.C;
-    ep.Z = a.Z;
-    ep.cols = a.cols;
-    ep.act = a.act;
-    const int64_t tiles = ceil_div(a.rows, 64) * ceil_div(a.cols, 64);
-    if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = launch_pdl(
-        unaligned_kernel, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, st, a.A.base,
-        a.A.mn_major ? 1 : a.A.ld, a.A.mn_major ? a.A.ld : 1, a.B.base,
-        a.B.mn_major ? 1 : a.B.ld, a.B.mn_major ? a.B.ld : 1, a.rows, a.depth, ep);
-    if (e == cudaSuccess) note_launch();
-    return e;
+// Products in one launch on the tensor cores, or (bf16 operands off 16-byte boundaries) each
+// without them.
+cudaError_t products(const GemmArgs *args, const GemmPlan *plans, int n, cudaStream_t st) {
+    bool on = true;
+    for (int i = 0; i < n; ++i)
+        on = on && aligned(args[i].A.base, 16) && aligned(args[i].B.base, 16);
+    if (on) return launch_gemm(args, plans, n, st);
+    for (int i = 0; i < n; ++i) {
+        const GemmArgs &a = args[i];
+        Epilogue ep{};
+        ep.bias = a.bias;
+        ep.R = a.R;
+        ep.C = a.C;
+        ep.Z = a.Z;
+        ep.cols = a.cols;
+        ep.act = a.act;
+        const int64_t tiles = ceil_div(a.rows, 64) * ceil_div(a.cols, 64);
+        if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
+        const cudaError_t e = launch_pdl(
+            unaligned_kernel, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, st, a.A.base,
+            a.A.mn_major ? 1 : a.A.ld, a.A.mn_major ? a.A.ld : 1, a.B.base,
+            a.B.mn_major ? 1 : a.B.ld, a.B.mn_major ? a.B.ld : 1, a.rows, a.depth, ep);
+        if (e != cudaSuccess) return e;
+        note_launch();
+    }
+    return cudaSuccess;
 }
 
 template <typename T>
@@ -470,7 +478,7 @@ cudaError_t linear_t(const LinearArgs &a, void *ws, cudaStream_t st) {
     g.Z = a.Z;
     g.part = ws_ptr<float>(ws, L.part);
     g.err = ws_ptr<uint32_t>(ws, 0);
-    return product(g, st);
+    return products(&g, L.plan, 1, st);
 }
 
 template <typename T>
@@ -485,8 +493,8 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
     // G, with its column sums from the values before they are rounded to an operand, and the
     // other operands: one launch
     StageJobs jobs{};
-    const bool products = a.dX != nullptr || a.dW != nullptr;
-    const bool write = products && (L.stage_m || a.act != FK_ACT_NONE);
+    const bool any = a.dX != nullptr || a.dW != nullptr;
+    const bool write = any && (L.stage_m || a.act != FK_ACT_NONE);
     bool join = false;
     if (write || a.db) {
         StageJob s{};
@@ -513,30 +521,31 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         note_launch();
     }
-    GemmArgs g{};
-    g.dtype = a.dtype;
-    g.act = FK_ACT_NONE;
-    g.cols = a.d;
-    g.part = ws_ptr<float>(ws, L.part);
-    g.err = ws_ptr<uint32_t>(ws, 0);
-    g.A.base = write ? ws_ptr<uint16_t>(ws, L.g) : static_cast<const uint16_t *>(a.dY);
-    g.A.ld = write ? L.ldm : a.m;
-    if (a.dX) {
-        g.B = W;
-        g.rows = a.N;
-        g.depth = a.m;
-        g.C = a.dX;
-        if ((e = product(g, st)) != cudaSuccess) return e;
-    }
-    if (a.dW) {
-        g.A.mn_major = true;
-        g.B = X;
-        g.rows = a.m;
-        g.depth = a.N;
-        g.C = a.dW;
-        e = product(g, st);
-    }
-    return e;
+    // dX and dW in one launch (each cut the same way when asked for alone)
+    GemmArgs args[2] = {};
+    GemmPlan plans[2];
+    int n = 0;
+    auto add = [&](const GemmOperand &A, const GemmOperand &B, int64_t rows, int64_t depth,
+                   void *C, int which, size_t part) {
+        GemmArgs &g = args[n];
+        g.dtype = a.dtype;
+        g.A = A;
+        g.B = B;
+        g.rows = rows;
+        g.cols = a.d;
+        g.depth = depth;
+        g.act = FK_ACT_NONE;
+        g.C = C;
+        g.part = ws_ptr<float>(ws, part);
+        g.err = ws_ptr<uint32_t>(ws, 0);
+        plans[n++] = L.plan[which];
+    };
+    GemmOperand G{write ? ws_ptr<uint16_t>(ws, L.g) : static_cast<const uint16_t *>(a.dY),
+                  write ? L.ldm : a.m, false};
+    if (a.dX) add(G, W, a.N, a.m, a.dX, 0, L.part);
+    G.mn_major = true;
+    if (a.dW) add(G, X, a.m, a.N, a.dW, 1, L.part2);
+    return n > 0 ? products(args, plans, n, st) : cudaSuccess;
 }
 
 }  // namespace
