@@ -49,11 +49,6 @@ __device__ __forceinline__ float warp_sum_f(float v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_max_f(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
 
 // N consecutive elements as they lie in memory: 16 bytes, or one element where rows are not
 // multiples of 16 bytes.
@@ -114,7 +109,6 @@ struct Raw<T, 1> {
     T u;
     __device__ __forceinline__ void load(const T *p) { u = *p; }
     __device__ __forceinline__ void zero() { u = T(0); }
-    __device__ __forceinline__ void lowest() { head_store(&u, -INFINITY); }
     __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = head_load(&u); }
     static __device__ __forceinline__ void put(T *p, const float (&v)[1]) { head_store(p, v[0]); }
 };

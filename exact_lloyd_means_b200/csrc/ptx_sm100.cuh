@@ -77,14 +77,11 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
 // Wait until the phase with the given parity has completed.  Bounded: gives up (returns
 // false) once `*abort` is non-zero (when `abort` is not null) or `limit_ns` of wall time
 // has passed since the wait started; the caller then records the error and winds down.
-// sleep_ns > 0: pause that long between polls (waits that are not on the critical path).
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity,
-                                          const volatile uint32_t *abort, uint64_t limit_ns,
-                                          uint32_t sleep_ns = 0) {
+                                          const volatile uint32_t *abort, uint64_t limit_ns) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
-        if (sleep_ns) __nanosleep(sleep_ns);
         if (mbar_try_wait(bar, parity)) return true;
         if ((it & 15u) == 0) {
             if (abort != nullptr && *abort) return false;
