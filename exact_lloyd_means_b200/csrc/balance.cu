@@ -20,28 +20,31 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxStages = 8;         // slots of the ring of rows
 constexpr int kRingBytes = 48 << 10;  // its size: three blocks an SM
-constexpr int kOneBlockLabels = 1 << 15;  // counted by one block in one launch
-constexpr int kSharedCells = 12288;       // counters kept in shared memory (48 KB)
+// Labels counted by one block in one launch (8192 of 64 cells 3.0 us against 3.3 in two
+// launches, 16,384 4.9 against 3.8; but a launch costs the host more than 2).
+constexpr int kOneBlockLabels = 1 << 14;
+constexpr int kSharedCells = 12256;       // counters kept in shared memory (under 48 KB in all)
 
-// Counts of one run of rows: in shared memory, then (several blocks) added to the zeroed
-// totals; or, with so many cells that a block meets most of them at most once or twice, in
-// the totals at once, equal labels of a warp together.  Integer atomics: the order does not
-// change the sums.
+// Counts of one run of rows: in shared memory, in `copies` histograms (warp w adds to copy w
+// mod copies, so that warps meet less often on a popular cell), which are then added to the
+// zeroed totals; with more cells than fit there (copies = 0), in the totals at once, equal
+// labels of a warp together.  Integer atomics: the order does not change the sums.
 template <bool ONE>
 __global__ void __launch_bounds__(1024)
-    balance_counts_kernel(const int32_t *__restrict__ labels, int64_t N, int top, int K, int local,
-                          int32_t *__restrict__ counts, int32_t *__restrict__ rows) {
+    balance_counts_kernel(const int32_t *__restrict__ labels, int64_t N, int top, int K,
+                          int copies, int32_t *__restrict__ counts, int32_t *__restrict__ rows) {
     extern __shared__ int32_t hist[];
     __shared__ int32_t srows;
     pdl_wait();
     pdl_trigger();
-    if (local)
-        for (int k = threadIdx.x; k < K; k += blockDim.x) hist[k] = 0;
+    for (int k = threadIdx.x; k < copies * K; k += blockDim.x) hist[k] = 0;
     if (threadIdx.x == 0) srows = 0;
     __syncthreads();
     const int64_t i0 = N * blockIdx.x / gridDim.x, i1 = N * (blockIdx.x + 1) / gridDim.x;
+    int32_t *mine = copies > 0 ? hist + (threadIdx.x >> 5) % copies * K : nullptr;
     // every selection, four loads ahead
     const int64_t e = i1 * top, stride = blockDim.x;
+    int kept = 0;  // rows with any selection
     for (int64_t j0 = i0 * top; j0 < e; j0 += 4 * stride) {
         int32_t l[4];
 #pragma unroll
@@ -52,8 +55,9 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const bool in = l[u] >= 0 && l[u] < K;
-            if (local) {
-                if (in) atomicAdd(hist + l[u], 1);
+            kept += top == 1 && in;
+            if (copies > 0) {
+                if (in) atomicAdd(mine + l[u], 1);
             } else {
                 const uint32_t same = __match_any_sync(0xffffffffu, in ? l[u] : -1);
                 if (in && (threadIdx.x & 31) == __ffs(same) - 1)
@@ -61,27 +65,40 @@ __global__ void __launch_bounds__(1024)
             }
         }
     }
-    // rows with any selection
-    int mine = 0;
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += stride) {
-        bool any = false;
-        for (int t = 0; t < top && !any; ++t) {
-            const int32_t l = labels[i * top + t];
-            any = l >= 0 && l < K;
+    for (int64_t r0 = i0; top > 1 && r0 < i1; r0 += 4 * stride) {
+        int32_t l[4];  // most rows show it in their first selection
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = r0 + u * stride + threadIdx.x;
+            l[u] = i < i1 ? labels[i * top] : -1;
         }
-        mine += any;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = r0 + u * stride + threadIdx.x;
+            bool any = l[u] >= 0 && l[u] < K;
+            for (int t = 1; t < top && !any && i < i1; ++t) {
+                const int32_t o = labels[i * top + t];
+                any = o >= 0 && o < K;
+            }
+            kept += any;
+        }
     }
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    if ((threadIdx.x & 31) == 0 && mine) atomicAdd(&srows, mine);
+    kept = __reduce_add_sync(0xffffffffu, kept);
+    if ((threadIdx.x & 31) == 0 && kept) atomicAdd(&srows, kept);
     __syncthreads();
-    if (ONE) {
-        for (int k = threadIdx.x; k < K; k += blockDim.x) counts[k] = hist[k];
-        if (threadIdx.x == 0) *rows = srows;
-    } else {
-        if (local)
-            for (int k = threadIdx.x; k < K; k += blockDim.x)
-                if (hist[k]) atomicAdd(counts + k, hist[k]);
-        if (threadIdx.x == 0 && srows) atomicAdd(rows, srows);
+    for (int k = threadIdx.x; k < K && copies > 0; k += blockDim.x) {
+        int32_t s = 0;
+        for (int c = 0; c < copies; ++c) s += hist[c * K + k];
+        if (ONE)
+            counts[k] = s;
+        else if (s)
+            atomicAdd(counts + k, s);
+    }
+    if (threadIdx.x == 0) {
+        if (ONE)
+            *rows = srows;
+        else if (srows)
+            atomicAdd(rows, srows);
     }
 }
 
@@ -602,9 +619,12 @@ int64_t balance_parts(int64_t N, int K) {
 cudaError_t launch_balance_counts(const int32_t *labels, int64_t N, int top, int K,
                                   int32_t *counts, int32_t *rows, cudaStream_t st) {
     cudaError_t e;
-    if (K <= kSharedCells && N * top <= kOneBlockLabels) {
-        e = launch_pdl(balance_counts_kernel<true>, dim3(1), dim3(1024), sizeof(int32_t) * K, st,
-                       labels, N, top, K, 1, counts, rows);
+    int copies = kSharedCells / K;
+    if (copies > 32) copies = 32;
+    const size_t smem = sizeof(int32_t) * copies * K;
+    if (copies > 0 && N * top <= kOneBlockLabels) {
+        e = launch_pdl(balance_counts_kernel<true>, dim3(1), dim3(1024), smem, st, labels, N, top,
+                       K, copies, counts, rows);
         if (e == cudaSuccess) note_launch();
         return e;
     }
@@ -616,9 +636,8 @@ cudaError_t launch_balance_counts(const int32_t *labels, int64_t N, int top, int
     if (N == 0) return e;
     int64_t g = ceil_div(N * top, 1024);
     if (g > 148) g = 148;
-    const int local = K <= kSharedCells && N * top / g >= 2 * static_cast<int64_t>(K);
-    e = launch_pdl(balance_counts_kernel<false>, dim3(static_cast<unsigned>(g)), dim3(1024),
-                   local ? sizeof(int32_t) * K : 0, st, labels, N, top, K, local, counts, rows);
+    e = launch_pdl(balance_counts_kernel<false>, dim3(static_cast<unsigned>(g)), dim3(1024), smem,
+                   st, labels, N, top, K, copies, counts, rows);
     if (e == cudaSuccess) note_launch();
     return e;
 }

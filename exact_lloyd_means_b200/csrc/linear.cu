@@ -9,6 +9,8 @@
 // nothing is transposed.  What this file adds is the staging of operands that TMA cannot
 // read as they lie (fp32 values as three bf16 planes; bf16 rows that are not multiples of 16
 // bytes), G with its column sums, and a kernel for a few rows, which only reads W.
+#include <type_traits>
+
 #include "gemm.cuh"
 
 namespace fk {
@@ -250,60 +252,84 @@ cudaError_t launch_stage(const StageJobs &jobs, cudaStream_t st) {
 }
 
 // ----------------------------------------------------------------- a few rows
-// Up to kFewRows rows of X: one warp per output column reads its row of W once and keeps a
-// sum per row of X (which stays in L1).  W is all the traffic.
-constexpr int kFewRows = 8;
+// A few rows of X: a block reads CW rows of W once, its four warps a quarter of the depth each,
+// and keeps a sum per row of X (which stays in L1) and column.  W is all the traffic.
+//
+// Where it is taken (us, this kernel / the tensor cores, replayed from a graph):
+//   fp32, up to 16 rows: 1 x 768 x 768 1.7 / 14.6, 8 x 768 x 4096 8.1 / 23.1, 16 x 4096 x 4096
+//   56 / 73 (the split of W costs the tensor cores more than its products);
+//   bf16, up to 4 rows: 1 x 768 x 768 1.6 / 6.2, 4 x 4096 x 4096 12.6 / 13.7; up to 8 where W
+//   has at most 2^20 elements: 8 x 768 x 768 4.1 / 6.1, but 8 x 768 x 4096 8.5 / 6.7.
+bool few_rows(int64_t N, int d, int m, fk_dtype dtype) {
+    if (dtype == FK_F32) return N <= 16;
+    return N <= 4 || (N <= 8 && static_cast<int64_t>(m) * d <= (1 << 20));
+}
 
-template <typename T, int NR>
+template <typename T, int NR, int CW>
 __global__ void __launch_bounds__(128)
     few_rows_kernel(const T *__restrict__ X, const T *__restrict__ W, int N, int d, int vec,
                     const Epilogue ep) {
     constexpr int V = kVec<T>;
+    __shared__ float red[4][NR * CW];
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (c >= ep.cols) return;
-    const T *w = W + c * d;
-    float s[NR] = {};
-    if (vec) {
-#pragma unroll 4
-        for (int64_t k = lane * V; k < d; k += 32 * V) {
-            float a[V];
-            unpack16(*reinterpret_cast<const uint4 *>(w + k), a);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * CW;
+    // (columns past the last are formed from the last row of W and not written)
+    const T *w[CW];
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                if (r < N) {
-                    float x[V];
-                    unpack16(*reinterpret_cast<const uint4 *>(X + static_cast<int64_t>(r) * d + k),
-                             x);
+    for (int c = 0; c < CW; ++c) w[c] = W + (c0 + c < ep.cols ? c0 + c : ep.cols - 1) * d;
+    float s[NR][CW] = {};
+    auto step = [&](int64_t k, auto width) {
+        constexpr int L = decltype(width)::value;
+        Raw<T, L> raw[CW];
 #pragma unroll
-                    for (int j = 0; j < V; ++j) s[r] += a[j] * x[j];
-                }
+        for (int c = 0; c < CW; ++c) raw[c].load(w[c] + k);
+        float a[CW][L];
+#pragma unroll
+        for (int c = 0; c < CW; ++c) raw[c].get(a[c]);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            if (r < N) {
+                Raw<T, L> u;
+                u.load(X + static_cast<int64_t>(r) * d + k);
+                float x[L];
+                u.get(x);
+#pragma unroll
+                for (int c = 0; c < CW; ++c)
+#pragma unroll
+                    for (int j = 0; j < L; ++j) s[r][c] += a[c][j] * x[j];
             }
         }
+    };
+    if (vec) {
+#pragma unroll 2
+        for (int64_t k = threadIdx.x * V; k < d; k += 128 * V)
+            step(k, std::integral_constant<int, V>{});
     } else {
-#pragma unroll 4
-        for (int64_t k = lane; k < d; k += 32) {
-            const float a = head_load(w + k);
-#pragma unroll
-            for (int r = 0; r < NR; ++r)
-                if (r < N) s[r] += a * head_load(X + static_cast<int64_t>(r) * d + k);
-        }
+#pragma unroll 2
+        for (int64_t k = threadIdx.x; k < d; k += 128) step(k, std::integral_constant<int, 1>{});
     }
 #pragma unroll
-    for (int r = 0; r < NR; ++r) s[r] = warp_sum_f(s[r]);
-    const float b = ep.bias != nullptr ? ep.bias[c] : 0.f;
+    for (int r = 0; r < NR; ++r)
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-        if (lane == r && r < N) {
-            const int64_t o = r * ep.cols + c;
-            const float z = __fadd_rn(s[r], b);
-            const float res = ep.R != nullptr ? head_load(static_cast<const T *>(ep.R) + o) : 0.f;
-            if (ep.Z != nullptr) head_store(static_cast<T *>(ep.Z) + o, z);
-            head_store(static_cast<T *>(ep.C) + o, __fadd_rn(act_value(z, ep.act), res));
+        for (int c = 0; c < CW; ++c) {
+            if (r < N) s[r][c] = warp_sum_f(s[r][c]);
+            if (lane == 0) red[warp][r * CW + c] = s[r][c];
         }
-    }
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) >= NR * CW) return;
+    const int r = threadIdx.x / CW;
+    const int64_t col = c0 + threadIdx.x % CW;
+    if (r >= N || col >= ep.cols) return;
+    float z = red[0][threadIdx.x];
+#pragma unroll
+    for (int t = 1; t < 4; ++t) z += red[t][threadIdx.x];
+    z = __fadd_rn(z, ep.bias != nullptr ? ep.bias[col] : 0.f);
+    const int64_t o = r * ep.cols + col;
+    const float res = ep.R != nullptr ? head_load(static_cast<const T *>(ep.R) + o) : 0.f;
+    if (ep.Z != nullptr) head_store(static_cast<T *>(ep.Z) + o, z);
+    head_store(static_cast<T *>(ep.C) + o, __fadd_rn(act_value(z, ep.act), res));
 }
 
 template <typename T>
@@ -317,13 +343,26 @@ cudaError_t launch_few_rows(const LinearArgs &a, cudaStream_t st) {
     ep.act = a.act;
     const int vec = a.d % kVec<T> == 0 && aligned(a.X, 16) && aligned(a.W, 16);
     const T *X = static_cast<const T *>(a.X), *W = static_cast<const T *>(a.W);
-    const dim3 grid(static_cast<unsigned>(ceil_div(a.m, 4)));
     const int N = static_cast<int>(a.N);
-    const auto k = N == 1 ? few_rows_kernel<T, 1>
-                          : (N <= 4 ? few_rows_kernel<T, 4> : few_rows_kernel<T, kFewRows>);
-    const cudaError_t e = launch_pdl(k, grid, dim3(128), 0, st, X, W, N, a.d, vec, ep);
-    if (e == cudaSuccess) note_launch();
-    return e;
+    auto launch = [&](auto kernel, int columns) {
+        const cudaError_t e =
+            launch_pdl(kernel, dim3(static_cast<unsigned>(ceil_div(a.m, columns))), dim3(128), 0,
+                       st, X, W, N, a.d, vec, ep);
+        if (e == cudaSuccess) note_launch();
+        return e;
+    };
+    // four columns a block from 1024 on (4 x 768 x 4096 bf16 5.3 against 6.3 with one), one
+    // where the GPU would stay empty (8 x 4096 x 100 bf16 4.1 against 9.2)
+    auto rows = [&](auto columns) {
+        constexpr int CW = decltype(columns)::value;
+        if (N == 1) return launch(few_rows_kernel<T, 1, CW>, CW);
+        if (N <= 2) return launch(few_rows_kernel<T, 2, CW>, CW);
+        if (N <= 4) return launch(few_rows_kernel<T, 4, CW>, CW);
+        if (N <= 8 || sizeof(T) == 2) return launch(few_rows_kernel<T, 8, CW>, CW);
+        return launch(few_rows_kernel<T, sizeof(T) == 4 ? 16 : 8, CW>, CW);
+    };
+    return a.m >= 1024 ? rows(std::integral_constant<int, 4>{})
+                       : rows(std::integral_constant<int, 1>{});
 }
 
 // ----------------------------------------------------------------- unaligned bf16 operands
@@ -396,7 +435,7 @@ LinearLayout linear_layout(int64_t N, int d, int m, fk_dtype dtype, bool backwar
         o += static_cast<size_t>(round_up(bytes, 256));
         return at;
     };
-    const bool few = !backward && N <= kFewRows;
+    const bool few = !backward && few_rows(N, d, m, dtype);
     L.x = take(L.stage_x && !few ? 2 * L.planes * N * L.ldd : 0);
     L.w = take(L.stage_x && !few ? 2 * L.planes * m * L.ldd : 0);
     if (backward) {
@@ -459,7 +498,7 @@ cudaError_t products(const GemmArgs *args, const GemmPlan *plans, int n, cudaStr
 
 template <typename T>
 cudaError_t linear_t(const LinearArgs &a, void *ws, cudaStream_t st) {
-    if (a.N <= kFewRows) return launch_few_rows<T>(a, st);
+    if (few_rows(a.N, a.d, a.m, a.dtype)) return launch_few_rows<T>(a, st);
     const LinearLayout L = linear_layout(a.N, a.d, a.m, a.dtype, false);
     GemmArgs g{};
     StageJobs jobs{};

@@ -195,7 +195,8 @@ def linear_tols(X, W, b, act, R, dtype):
     return y, z, hs * y.abs() + ey * (1 + hs), hs * z.abs() + ez * (1 + hs)
 
 
-LIN_SIZES = [(1, 1, 1), (1, 16, 16), (3, 5, 7), (1, 768, 768), (8, 768, 129), (9, 64, 1000),
+LIN_SIZES = [(1, 1, 1), (1, 16, 16), (3, 5, 7), (2, 4096, 30), (5, 600, 33), (11, 333, 50),
+             (16, 512, 70), (1, 768, 768), (8, 768, 129), (9, 64, 1000),
              (17, 100, 300), (50, 768, 256), (127, 129, 131), (128, 64, 256), (300, 257, 513),
              (257, 1000, 65), (1000, 72, 4), (4, 4096, 40), (64, 2048, 64), (130, 4104, 520),
              (1025, 320, 1100)]
@@ -367,7 +368,8 @@ def balance_tols(S, labels, counts, n, scale, coef, dtype):
 
 BAL_SIZES = [(1, 1, 1), (1, 2, 1), (5, 3, 2), (100, 8, 2), (257, 64, 2), (1000, 60, 3),
              (33, 129, 8), (500, 256, 4), (65, 1000, 1), (40, 2048, 2), (9, 4097, 1),
-             (20, 8192, 8), (3, 70000, 1), (3000, 16, 1), (10, 40000, 300)]
+             (20, 8192, 8), (3, 70000, 1), (3000, 16, 1), (10, 40000, 300),
+             (40000, 4096, 1), (6, 12288, 2), (7, 12256, 1), (30000, 6, 3)]
 
 
 def make_labels(N, K, top, seed, pad):
