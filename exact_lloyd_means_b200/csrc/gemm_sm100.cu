@@ -371,7 +371,9 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
             // (by value and by fixed index: a reference picked here is read from memory again
             // at every use)
             const bool j = u >= jobs.second;
-            const Epilogue ep = j ? jobs.ep[1] : jobs.ep[0];
+            Epilogue ep = j ? jobs.ep[1] : jobs.ep[0];
+            const float *bias = ep.bias;
+            if (NP == 1) ep.bias = nullptr;  // (added here)
             const int64_t rows = j ? jobs.shape[1].rows : jobs.shape[0].rows;
             const int bvec = j ? jobs.bvec[1] : jobs.bvec[0];
             float *part = j ? jobs.part[1] : jobs.part[0];
@@ -392,17 +394,22 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
                         Raw<float, 8>::put(dst + j, o);
                     }
                 } else if constexpr (OV > 1) {
-                    float z[32 / OV][OV];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) z[j / OV][j % OV] = v[j];
-                    Pieces o{(r0 + lane) * ep.cols + col, OV, col, OV, 0u};
-                    const int64_t left = (ep.cols - col) / OV;  // pieces before the last column
-                    if (r0 + lane >= rows || left <= 0) return;
-                    if (left >= 32 / OV) {
-                        epilogue_pieces<T, OV, true>(ep, o, bvec, z);
+                    if constexpr (NP == 3) {
+                        if (r0 < rows && col < ep.cols)
+                            epilogue_warp_f32<OV>(ep, r0, rows, col, bvec, lane, v);
                     } else {
-                        o.in = (1u << left) - 1u;
-                        epilogue_pieces<T, OV, false>(ep, o, bvec, z);
+                        float z[32 / OV][OV];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) z[j / OV][j % OV] = v[j];
+                        Pieces o{(r0 + lane) * ep.cols + col, OV, col, OV, 0u};
+                        const int64_t left = (ep.cols - col) / OV;  // pieces before the last column
+                        if (r0 + lane >= rows || left <= 0) return;
+                        if (left >= 32 / OV) {
+                            epilogue_pieces<T, OV, true>(ep, o, bvec, z);
+                        } else {
+                            o.in = (1u << left) - 1u;
+                            epilogue_pieces<T, OV, false>(ep, o, bvec, z);
+                        }
                     }
                 } else {  // turned in shared memory: thread = column, so that rows are coalesced
 #pragma unroll
@@ -422,6 +429,27 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
                     __syncwarp();
                 }
             };
+            // bf16: the bias of columns c0 + 32 c .. + 31, read while the columns before are
+            // still in TMEM; behind their stores it would wait for them in the load and store
+            // unit.  10000 x 768 of depth 4096: 52 us, 54 with the read in the epilogue; 65536 x
+            // 128 of depth 1024: 48 and 55.  In fp32 the registers for it spill: 182 and 162.
+            [[maybe_unused]] float b[32];
+            [[maybe_unused]] auto fetch_bias = [&](int c) {
+                if (bias == nullptr) return;
+                const int64_t col = c0 + c * 32;
+                if (bvec && col + 32 <= ep.cols) {
+                    load_params<32>(bias + col, 1, b);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) b[j] = col + j < ep.cols ? bias[col + j] : 0.f;
+                }
+            };
+            [[maybe_unused]] auto add_bias = [&](float (&v)[32]) {
+                if (bias == nullptr) return;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __fadd_rn(v[j], b[j]);
+            };
+            if (NP == 1 && un.part < 0) fetch_bias(0);
             auto wait_acc = [&]() -> bool {
                 uint32_t good = 0;
                 if (lane == 0)
@@ -456,6 +484,10 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
                     float v[32];
                     ptx::tmem_ld32_sync(tb + c * 32, v);
                     if (c == C - 1) release();
+                    if (un.part < 0) {
+                        add_bias(v);
+                        if (c + 1 < C) fetch_bias(c + 1);
+                    }
                     finish(c, v);
                 }
                 ++it;
