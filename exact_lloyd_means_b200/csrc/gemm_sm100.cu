@@ -78,6 +78,7 @@ struct GemmShape {
     int splits;
     int a_mn, b_mn;
     int64_t tiles_r, tiles_c;
+    uint64_t inv_band;   // 2^64 / (tiles of a band), rounded down
     int64_t full, tail;  // tiles with the whole depth, tiles with their depth cut
 };
 
@@ -92,15 +93,27 @@ struct alignas(64) GemmJobs {
 };
 
 // Tile t in the order of work: bands of kBandRows row tiles, rows fastest within a band, so that
-// the tiles running side by side share their operands in L2.
-__host__ __device__ __forceinline__ void tile_of(const GemmShape &s, int64_t t, int64_t &tr,
-                                                 int64_t &tc) {
+// the tiles running side by side share their operands in L2.  Each warp works this out before
+// every tile, and where the depth is short nothing hides what it takes: without its two 64-bit
+// divisions 65536 x 128 x 4096 takes 170 us, with them 173.
+__device__ __forceinline__ void tile_of(const GemmShape &s, int64_t t, int64_t &tr, int64_t &tc) {
     const int64_t per_band = kBandRows * s.tiles_c;
-    const int64_t band = t / per_band, in = t - band * per_band;
+    // (t < 2^34, so this is the quotient or one less)
+    int64_t band = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(t), s.inv_band));
+    int64_t in = t - band * per_band;
+    if (in >= per_band) {
+        ++band;
+        in -= per_band;
+    }
     const int64_t left = s.tiles_r - band * kBandRows;
-    const int64_t h = left < kBandRows ? left : kBandRows;
-    tc = in / h;
-    tr = band * kBandRows + (in - tc * h);
+    if (left >= kBandRows) {
+        tc = in / kBandRows;
+        tr = band * kBandRows + in % kBandRows;
+    } else {  // (a band has fewer than 2^29 tiles)
+        const uint32_t i = static_cast<uint32_t>(in), h = static_cast<uint32_t>(left);
+        tc = i / h;
+        tr = band * kBandRows + i % h;
+    }
 }
 
 // Unit u: its chunks of the depth, which part of it they are (0 of 1 for a whole one) ...
@@ -622,6 +635,7 @@ cudaError_t launch_cfg(const GemmArgs *args, const GemmPlan *plans, int n, cudaS
         s.b_mn = a.B.mn_major;
         s.tiles_r = ceil_div(a.rows, kBM * CG);
         s.tiles_c = ceil_div(a.cols, BN);
+        s.inv_band = ~uint64_t(0) / static_cast<uint64_t>(kBandRows * s.tiles_c);
         s.full = p.full;
         s.tail = p.tail;
         jobs.bvec[i] = aligned(a.bias, 16);
