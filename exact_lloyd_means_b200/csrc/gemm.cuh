@@ -46,7 +46,53 @@ void gemm_plan(const GemmSize *sizes, int n, fk_dtype dtype, GemmPlan *plans);
 inline size_t gemm_part_bytes(const GemmPlan &p) {
     return p.splits > 1 ? sizeof(float) * p.tail * p.splits * p.tile() : 0;
 }
-cudaError_t launch_gemm(const GemmArgs *args, const GemmPlan *plans, int n, cudaStream_t st);
+
+// Column sums to be finished: db = the sum of the parts, each of `cols`.
+struct ColSums {
+    const float *part;
+    float *db;
+    int parts, cols;
+};
+
+// `sums`: finished by the launch that joins cut products, so only where there is one (or NULL
+// db: none).
+cudaError_t launch_gemm(const GemmArgs *args, const GemmPlan *plans, int n, const ColSums &sums,
+                        cudaStream_t st);
+
+// Columns 32 b .. 32 b + 31 of the sums by T threads: 32 runs of parts side by side, then the
+// runs in a tree, whatever T is.
+template <int T>
+__device__ __forceinline__ void join_columns(const ColSums &s, int b, float (&red)[32][33]) {
+    const int x = threadIdx.x & 31;
+    const int64_t c = static_cast<int64_t>(b) * 32 + x;
+    constexpr int Y = 32 * 32 / T, H = T / 32;  // runs of a thread: y, y + H, ...
+    const int y0 = threadIdx.x >> 5;
+    float v[Y] = {};
+    if (c < s.cols) {
+        const float *part = s.part + c;
+        const auto at = [&](int p) { return static_cast<int64_t>(p) * s.cols; };
+        const int whole = s.parts / 32 * 32;
+#pragma unroll(8 / Y)
+        for (int p = y0; p < whole; p += 32)
+#pragma unroll
+            for (int i = 0; i < Y; ++i) v[i] += part[at(p + i * H)];
+#pragma unroll
+        for (int i = 0; i < Y; ++i) {
+            const int p = whole + y0 + i * H;
+            if (p < s.parts) v[i] += part[at(p)];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < Y; ++i) red[y0 + i * H][x] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < Y; ++i) {
+        const int y = y0 + i * H;
+        const float t = warp_sum_f(red[x][y]);  // the runs of column y
+        const int64_t o = static_cast<int64_t>(b) * 32 + y;
+        if (x == 0 && o < s.cols) s.db[o] = t;
+    }
+}
 
 // ----------------------------------------------------------------- epilogue
 // One branch for all the values, which keeps their chains of dependent instructions side by

@@ -558,11 +558,18 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
 
 // Join the partial products of the tail tiles, in order, and apply the epilogue.  Block (x,
 // y): rows of tail tile x, those of the first product (`split0` of them) before the second's.
+// Behind all `tiles`, blocks of column sums.
 template <typename T, int V>
 __global__ void __launch_bounds__(256)
-    gemm_join_kernel(const __grid_constant__ GemmJobs jobs, int split0, int tile_rows, int bn) {
+    gemm_join_kernel(const __grid_constant__ GemmJobs jobs, int split0, int tiles, int tile_rows,
+                     int bn, const ColSums sums) {
+    __shared__ float red[32][33];
     pdl_wait();
     pdl_trigger();
+    if (static_cast<int>(blockIdx.x) >= tiles) {
+        if (blockIdx.y == 0) join_columns<256>(sums, blockIdx.x - tiles, red);
+        return;
+    }
     const int job = static_cast<int>(blockIdx.x) >= split0;
     const int64_t tile = static_cast<int64_t>(blockIdx.x) - (job ? split0 : 0);
     const GemmShape &s = jobs.shape[job];
@@ -609,7 +616,8 @@ bool operand_map(CUtensorMap *m, const GemmOperand &o, int64_t outer, int64_t in
 }
 
 template <int CG, int BN, typename T, int OV>
-cudaError_t launch_cfg(const GemmArgs *args, const GemmPlan *plans, int n, cudaStream_t st) {
+cudaError_t launch_cfg(const GemmArgs *args, const GemmPlan *plans, int n, const ColSums &sums,
+                       cudaStream_t st) {
     using Cfg = GemmCfg<CG, BN, kPlanes<T>, OV>;
     auto kernel = gemm_kernel<CG, BN, T, OV>;
     static std::atomic<uint64_t> smem_set{0};
@@ -675,24 +683,28 @@ cudaError_t launch_cfg(const GemmArgs *args, const GemmPlan *plans, int n, cudaS
         const int64_t want = ceil_div(static_cast<int64_t>(device_sm_count()) * 8, tiles);
         const int64_t most = int64_t(kBM) * CG * BN / JV / 256;
         e = launch_pdl(gemm_join_kernel<T, JV>,
-                       dim3(static_cast<unsigned>(tiles),
+                       dim3(static_cast<unsigned>(tiles + ceil_div(sums.db ? sums.cols : 0, 32)),
                             static_cast<unsigned>(want < most ? want : most)),
-                       dim3(256), 0, st, jobs, static_cast<int>(joined[0]), kBM * CG, BN);
+                       dim3(256), 0, st, jobs, static_cast<int>(joined[0]),
+                       static_cast<int>(tiles), kBM * CG, BN, sums);
         if (e == cudaSuccess) note_launch();
     }
     return e;
 }
 
 template <typename T, int OV>
-cudaError_t launch_v(const GemmArgs *a, const GemmPlan *p, int n, cudaStream_t st) {
+cudaError_t launch_v(const GemmArgs *a, const GemmPlan *p, int n, const ColSums &sums,
+                     cudaStream_t st) {
     // (fp32: two accumulators a tile, so half the columns)
-    if (p->cg == 2) return launch_cfg<2, 256 / (kPlanes<T> == 3 ? 2 : 1), T, OV>(a, p, n, st);
-    if (p->bn == 128) return launch_cfg<1, 128, T, OV>(a, p, n, st);
-    return launch_cfg<1, 64, T, OV>(a, p, n, st);
+    constexpr int kPairCols = 256 / (kPlanes<T> == 3 ? 2 : 1);
+    if (p->cg == 2) return launch_cfg<2, kPairCols, T, OV>(a, p, n, sums, st);
+    if (p->bn == 128) return launch_cfg<1, 128, T, OV>(a, p, n, sums, st);
+    return launch_cfg<1, 64, T, OV>(a, p, n, sums, st);
 }
 
 template <typename T>
-cudaError_t launch_t(const GemmArgs *a, const GemmPlan *p, int n, cudaStream_t st) {
+cudaError_t launch_t(const GemmArgs *a, const GemmPlan *p, int n, const ColSums &sums,
+                     cudaStream_t st) {
     constexpr int V = kVec<T>;
     auto rows_on = [&](int v) {
         const size_t b = v * sizeof(T);
@@ -702,9 +714,9 @@ cudaError_t launch_t(const GemmArgs *a, const GemmPlan *p, int n, cudaStream_t s
                  aligned(a[i].R, b);
         return ok;
     };
-    if (rows_on(2 * V)) return launch_v<T, 2 * V>(a, p, n, st);
-    if (rows_on(V)) return launch_v<T, V>(a, p, n, st);
-    return launch_v<T, 1>(a, p, n, st);
+    if (rows_on(2 * V)) return launch_v<T, 2 * V>(a, p, n, sums, st);
+    if (rows_on(V)) return launch_v<T, V>(a, p, n, sums, st);
+    return launch_v<T, 1>(a, p, n, sums, st);
 }
 
 }  // namespace
@@ -769,9 +781,10 @@ void gemm_plan(const GemmSize *sizes, int n, fk_dtype dtype, GemmPlan *plans) {
     }
 }
 
-cudaError_t launch_gemm(const GemmArgs *args, const GemmPlan *plans, int n, cudaStream_t st) {
-    return args[0].dtype == FK_F32 ? launch_t<float>(args, plans, n, st)
-                                   : launch_t<uint16_t>(args, plans, n, st);
+cudaError_t launch_gemm(const GemmArgs *args, const GemmPlan *plans, int n, const ColSums &sums,
+                        cudaStream_t st) {
+    return args[0].dtype == FK_F32 ? launch_t<float>(args, plans, n, sums, st)
+                                   : launch_t<uint16_t>(args, plans, n, sums, st);
 }
 
 }  // namespace fk

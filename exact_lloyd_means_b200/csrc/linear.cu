@@ -187,25 +187,16 @@ __global__ void __launch_bounds__(256) stage_kernel(const __grid_constant__ Stag
     }
 }
 
-// db = the sum of the parts: 32 columns a block, 32 runs of parts side by side.
-__global__ void __launch_bounds__(1024)
-    col_join_kernel(const float *__restrict__ part, int parts, int cols, float *__restrict__ db) {
+// The column sums in a launch of their own.  A join of cut products takes up to kJoinParts
+// parts along instead: the gradients of 1001 x 300 x 129 fp32 (126 parts) take 16.8 us so and 18.8
+// with the launch, 3000 x 768 x 768 bf16 (375) 23.8 and 26.3, but 8192 x 768 x 768 (888 parts,
+// which 1024 threads read faster than 256) 48.8 and 47.5.
+constexpr int kJoinParts = 400;
+__global__ void __launch_bounds__(1024) col_join_kernel(const ColSums s) {
     __shared__ float red[32][33];
     pdl_wait();
     pdl_trigger();
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + x;
-    float s = 0.f;
-    if (c < cols) {
-#pragma unroll 8
-        for (int p = y; p < parts; p += 32) s += part[static_cast<int64_t>(p) * cols + c];
-    }
-    red[y][x] = s;
-    __syncthreads();
-    // warp y sums the runs of column y
-    s = warp_sum_f(red[x][y]);
-    const int64_t o = static_cast<int64_t>(blockIdx.x) * 32 + y;
-    if (x == 0 && o < cols) db[o] = s;
+    join_columns<1024>(s, blockIdx.x, red);
 }
 
 // Threads across a row, 8 columns each: whole rows where they fit (memory likes long runs: at
@@ -470,11 +461,15 @@ GemmOperand operand(StageJobs &jobs, const void *src, int64_t rows, int cols, bo
 
 // Products in one launch on the tensor cores, or (bf16 operands off 16-byte boundaries) each
 // without them.
-cudaError_t products(const GemmArgs *args, const GemmPlan *plans, int n, cudaStream_t st) {
+bool on_tensor_cores(const GemmArgs *args, int n) {
     bool on = true;
     for (int i = 0; i < n; ++i)
         on = on && aligned(args[i].A.base, 16) && aligned(args[i].B.base, 16);
-    if (on) return launch_gemm(args, plans, n, st);
+    return on;
+}
+cudaError_t products(const GemmArgs *args, const GemmPlan *plans, int n, const ColSums &sums,
+                     cudaStream_t st) {
+    if (on_tensor_cores(args, n)) return launch_gemm(args, plans, n, sums, st);
     for (int i = 0; i < n; ++i) {
         const GemmArgs &a = args[i];
         Epilogue ep{};
@@ -517,7 +512,7 @@ cudaError_t linear_t(const LinearArgs &a, void *ws, cudaStream_t st) {
     g.Z = a.Z;
     g.part = ws_ptr<float>(ws, L.part);
     g.err = ws_ptr<uint32_t>(ws, 0);
-    return products(&g, L.plan, 1, st);
+    return products(&g, L.plan, 1, ColSums{}, st);
 }
 
 template <typename T>
@@ -534,7 +529,7 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
     StageJobs jobs{};
     const bool any = a.dX != nullptr || a.dW != nullptr;
     const bool write = any && (L.stage_m || a.act != FK_ACT_NONE);
-    bool join = false;
+    ColSums sums{};
     if (write || a.db) {
         StageJob s{};
         s.src = a.dY;
@@ -545,8 +540,12 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
         s.out = write ? ws_ptr<uint16_t>(ws, L.g) : nullptr;
         s.ld = L.ldm;
         // a single run of rows has the sums themselves
-        join = a.db && stage_parts(a.N, a.m) > 1;
-        s.colpart = join ? ws_ptr<float>(ws, L.col) : a.db;
+        const int parts = stage_parts(a.N, a.m);
+        s.colpart = a.db;
+        if (a.db && parts > 1) {
+            s.colpart = ws_ptr<float>(ws, L.col);
+            sums = ColSums{s.colpart, a.db, parts, a.m};
+        }
         add_job(jobs, s);
     }
     GemmOperand W{}, X{};
@@ -554,12 +553,6 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
     if (a.dW) X = operand(jobs, a.X, a.N, a.d, L.stage_x, ws_ptr<uint16_t>(ws, L.x), true);
     cudaError_t e = launch_stage<T>(jobs, st);
     if (e != cudaSuccess) return e;
-    if (join) {
-        e = launch_pdl(col_join_kernel, dim3(static_cast<unsigned>(ceil_div(a.m, 32))), dim3(1024),
-                       0, st, ws_ptr<const float>(ws, L.col), stage_parts(a.N, a.m), a.m, a.db);
-        if (e != cudaSuccess) return e;
-        note_launch();
-    }
     // dX and dW in one launch (each cut the same way when asked for alone)
     GemmArgs args[2] = {};
     GemmPlan plans[2];
@@ -584,7 +577,16 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
     if (a.dX) add(G, W, a.N, a.m, a.dX, 0, L.part);
     G.mn_major = true;
     if (a.dW) add(G, X, a.m, a.N, a.dW, 1, L.part2);
-    return n > 0 ? products(args, plans, n, st) : cudaSuccess;
+    bool cut = false;
+    for (int i = 0; i < n; ++i) cut = cut || plans[i].splits > 1;
+    if (sums.db != nullptr && !(cut && sums.parts <= kJoinParts && on_tensor_cores(args, n))) {
+        e = launch_pdl(col_join_kernel, dim3(static_cast<unsigned>(ceil_div(a.m, 32))), dim3(1024),
+                       0, st, sums);
+        if (e != cudaSuccess) return e;
+        note_launch();
+        sums.db = nullptr;
+    }
+    return n > 0 ? products(args, plans, n, sums, st) : cudaSuccess;
 }
 
 }  // namespace
