@@ -582,7 +582,8 @@ cudaError_t loss_long(const BalanceArgs &b, const LossArgs &a, int *grid, cudaSt
 }
 
 // Up to 32 columns a thread (16 for one element at a time), and as few threads a row as that
-// allows: the sums over the threads cost about as much as ten columns.
+// allows: the sums over the threads cost about as much as ten columns.  65,536 bf16 rows: of 1024
+// 50 us (twice the threads: 63), of 2048 93 (114), of 4096 184 (203).
 template <typename T>
 cudaError_t loss_t(const BalanceArgs &b, const LossArgs &a, int *grid, cudaStream_t st) {
     constexpr int V = kVec<T>, C32 = 32 / V;

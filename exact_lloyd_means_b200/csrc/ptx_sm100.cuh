@@ -90,6 +90,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity,
     }
 }
 
+// ---------------------------------------------------------------- a thread's own copies
+
+// 16 bytes into shared memory; copies since the last commit are a group, and copies_wait<n>
+// returns when all but the last n groups of this thread have landed.
+__device__ __forceinline__ void copy16_async(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ---------------------------------------------------------------- clusters (CTA pairs)
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
