@@ -90,6 +90,13 @@ def test_layer_norm(fk, N, d, dtype):
     within(X2, y2, ln_tol(X, None, None, 1e-5, t)[0], "in place")
 
 
+@pytest.mark.parametrize("N,d", [(50001, 64), (45000, 256), (25003, 512), (20001, 760), (15000, 1024),
+                                 (7001, 2000), (3333, 4096), (1999, 8192)])
+def test_layer_norm_with_many_rows_a_block(fk, N, d):
+    """Every block takes many turns of rows, the last ones without a row for some groups."""
+    test_layer_norm(fk, N, d, "bf16")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_layer_norm_rows_of_one_value_and_special_values(fk, dtype):
     t = TYPES[dtype]
@@ -153,6 +160,11 @@ def test_layer_norm_backward(fk, N, d, dtype):
     within(dX, ref.layer_norm_backward(dY, X, None, m, r)[0],
            lnb_tols(dY, X, None, m, r, t)[0], "dX without gamma")
     assert torch.equal(dg2, dg) and torch.equal(db2, db)
+
+
+@pytest.mark.parametrize("N,d", [(2003, 1000), (1501, 1024), (1201, 1800), (900, 2048)])
+def test_layer_norm_backward_of_wide_fp32_rows(fk, N, d):
+    test_layer_norm_backward(fk, N, d, "f32")
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -267,6 +279,13 @@ def test_linear_backward(fk, N, d, m, dtype):
             fk.fk_linear_backward(dY, X, W, ws, act=act, Z=z, **{name: one})
             assert torch.equal(one, full), (name, act)
     assert fk.fk_get_device_error(ws) == fk.FK_OK
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,d,m", [(1001, 300, 129), (2900, 136, 100), (6500, 40, 768)])
+def test_linear_backward_with_many_parts_of_the_bias(fk, N, d, m, dtype):
+    """The bias gradient's parts are summed with the cut products' or by themselves."""
+    test_linear_backward(fk, N, d, m, dtype)
 
 
 @pytest.mark.parametrize("depth", [64, 700, 4096, 40000])
