@@ -736,6 +736,7 @@ cudaError_t backward_vectors(const LayerNormArgs &a, cudaStream_t st, int *parts
         if (a.d <= 128 * 16) return backward_ring<T, C16, 128>(a, st, parts);
     }
     if (a.d <= 256 * 16) return backward_ring<T, C16, 256>(a, st, parts);
+    if (a.d <= 256 * 32) return backward_ring<T, 2 * C16, 256>(a, st, parts);
     return backward_long<T>(a, st, parts);
 }
 
