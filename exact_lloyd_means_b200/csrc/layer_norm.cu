@@ -411,8 +411,9 @@ __global__ void __launch_bounds__(kThreads)
             phase ^= 1u;
         }
         if (dX != nullptr && row) {
-            const float ra = -r * a * inv, rb = -r * b * inv;
-            const F2 ra2 = f2(ra, ra), rb2 = f2(rb, rb);
+            // (as the formula has it: r w - r mean(w) would not be 0 where w is its mean)
+            const float na = -a * inv, nb = -b * inv;
+            const F2 na2 = f2(na, na), nb2 = f2(nb, nb);
             T *o = dX + i * d + t * V;
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kThreads)
                     F2 v[H];
 #pragma unroll
                     for (int k = 0; k < H; ++k)
-                        v[k] = fma2(rr, w[n][k], fma2(rb2, h[n][k], ra2));
+                        v[k] = mul2(rr, fma2(nb2, h[n][k], add2(w[n][k], na2)));
                     *reinterpret_cast<uint4 *>(o + n * TPR * V) = pack2(v);
                 }
             }
@@ -501,11 +502,11 @@ __global__ void __launch_bounds__(kThreads)
         group_sum2<TPR>(a, b, red, slot);
         slot ^= 1;
         if (dX != nullptr && i < N) {
-            const float ra = -rr * a * inv, rb = -rr * b * inv;
+            const float ma = a * inv, mb = b * inv;
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
                 const int j = n * TPR + t;
-                if (j < d) head_store(dX + i * d + j, rr * w[n] + (rb * h[n] + ra));
+                if (j < d) head_store(dX + i * d + j, rr * (__fsub_rn(w[n], ma) - mb * h[n]));
             }
         }
     }

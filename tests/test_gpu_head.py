@@ -162,6 +162,23 @@ def test_layer_norm_backward(fk, N, d, dtype):
     assert torch.equal(dg2, dg) and torch.equal(db2, db)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [1, 64])
+def test_layer_norm_backward_of_rows_without_a_gradient(fk, d, dtype):
+    """One column, or columns that all have the same w and no variance: w - mean(w) and h are
+    exactly 0, and so is dX."""
+    t = TYPES[dtype]
+    X = rnd((70, 1), t, 1, shift=0.5).expand(70, d).contiguous()
+    dY = rnd((70, 1), t, 2).expand(70, d).contiguous()
+    gamma = torch.full((d,), 0.7, device="cuda")
+    mean, rstd = X[:, 0].float().contiguous(), torch.full((70,), 1e-5 ** -0.5, device="cuda")
+    for g in (None, gamma):
+        dX = torch.full_like(X, float("nan"))
+        fk.fk_layer_norm_backward(dY, X, g, mean, rstd, dX, None, None,
+                                  fk.layer_norm_backward_workspace(70, d, t))
+        assert torch.all(dX == 0)
+
+
 @pytest.mark.parametrize("N,d", [(2003, 1000), (1501, 1024), (1201, 1800), (900, 2048)])
 def test_layer_norm_backward_of_wide_fp32_rows(fk, N, d):
     test_layer_norm_backward(fk, N, d, "f32")
@@ -286,6 +303,12 @@ def test_linear_backward(fk, N, d, m, dtype):
 def test_linear_backward_with_many_parts_of_the_bias(fk, N, d, m, dtype):
     """The bias gradient's parts are summed with the cut products' or by themselves."""
     test_linear_backward(fk, N, d, m, dtype)
+
+
+@pytest.mark.parametrize("N,d,m", [(135000, 40, 24), (131200, 128, 100)])
+def test_linear_backward_bf16_over_very_many_rows(fk, N, d, m):
+    """dW's depth is past what one accumulation takes."""
+    test_linear_backward(fk, N, d, m, "bf16")
 
 
 @pytest.mark.parametrize("depth", [64, 700, 4096, 40000])
