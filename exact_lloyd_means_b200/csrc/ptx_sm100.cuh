@@ -90,6 +90,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity,
     }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // ---------------------------------------------------------------- a thread's own copies
 
 // 16 bytes into shared memory; copies since the last commit are a group, and copies_wait<n>
