@@ -8,9 +8,11 @@
 //     two accumulators in tensor memory, so that a tile's epilogue overlaps the next tile's
 //     products; warps 2..9: epilogue, two groups of four warps, half the columns each.  A
 //     thread has one row of the tile and takes 32 columns at a time; it reads and writes
-//     them in whole 32-byte sectors.  Nothing passes through shared memory, whose bandwidth
-//     the operands take (128 x 64 by 256 x 64 a chunk written and read): staging the tile
-//     there as fp32 took 92 us where this takes 73 (10,000 x 768 x 4096, GELU, both outputs);
+//     them in whole 32-byte sectors (fp32 threads exchange theirs first, so that a store covers
+//     64 or 128 bytes of a row).  Only columns that do not start on 16 bytes pass through shared
+//     memory, whose bandwidth the operands take (128 x 64 by 256 x 64 a chunk written and
+//     read): staging the tile there as fp32 took 92 us where this takes 71 (10,000 x 768 x
+//     4096, GELU, both outputs);
 //   * either operand may be stored along the depth (K-major) or along its rows (MN-major):
 //     both are 128-byte-swizzled TMA boxes, and the MMA descriptors say which.  So the three
 //     products of a linear layer and its gradients read their operands as they lie;
