@@ -471,9 +471,9 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
                 for (int j = 0; j < 32; ++j) v[j] = __fadd_rn(v[j], b[j]);
             };
             if (kBiasAhead && un.part < 0) fetch_bias(0);
-            // Where tiles follow one another fast, the next one's residual is brought into L2.  65536
-            // x 1024 of depth 128, bf16: 76 us, 86 without; fp32 204 and 218; but 10000 x 4096 of
-            // depth 1536 103 and 101, and 2500 x 4096 of depth 768 in fp32 98 and 97.
+            // Where tiles follow one another fast, the next one's residual is brought into L2.
+            // 65536 x 1024 of depth 128, bf16: 76 us, 86 without; fp32 202 and 218; but 10000 x
+            // 4096 of depth 1536 103 and 101, and 2500 x 4096 of depth 768 in fp32 98 and 97.
             constexpr int kAhead = 12 / NP;  // chunks of the depth
             if (ep.R != nullptr && u + step < jobs.units && un.k1 - un.k0 <= kAhead) {
                 const bool jn = u + step >= jobs.second;

@@ -299,6 +299,13 @@ def test_linear_backward(fk, N, d, m, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,d,m", [(20001, 64, 520), (21000, 40, 333), (9000, 200, 1032)])
+def test_linear_with_many_tiles_a_block(fk, N, d, m, dtype):
+    """Every block takes several tiles of a short depth."""
+    test_linear(fk, N, d, m, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("N,d,m", [(1001, 300, 129), (2900, 136, 100), (6500, 40, 768)])
 def test_linear_backward_with_many_parts_of_the_bias(fk, N, d, m, dtype):
     """The bias gradient's parts are summed with the cut products' or by themselves."""
