@@ -510,6 +510,95 @@ def test_balance_rows_that_masks_leave_empty(fk, K, dtype):
     assert float(dS[2].float().abs().max()) <= 8 * U * K / 5
 
 
+def balance_difference_tols(S, labels, counts, n, scale, coef, dtype):
+    """Bounds that know differences of scores only.  x = scale (s - max) is formed in four
+    roundings (the difference, log2(e), its product with the scale, the product), so it is off by
+    4 u |x|; a warp's maximum in between splits x in two parts of that kind.  2^x is within 4 u,
+    twice where the warps' sums are joined; the sum of K terms over at least 16 lanes K / 16 u and
+    its reciprocal a few.  A probability under 2^-126 may be 0, which takes up to 2^-125 from p and,
+    as the shares add up to at most 1, from t.  An output is rounded to a multiple of its type's
+    least subnormal, and two of its factors to one of fp32's."""
+    K = S.shape[1]
+    kept = ref._kept(labels, K)[2][:, None]
+    x = torch.where(kept, scale * S.double(), torch.zeros((), dtype=torch.float64, device="cuda"))
+    x = x - x.max(1, keepdim=True).values
+    p = torch.softmax(x, 1) * kept
+    ep = 4 * U * torch.where(p > 0, -x, torch.zeros_like(x))
+    ep = ep + (p * ep).sum(1, keepdim=True) + U * (K / 16 + 32)
+    f = counts.double() / (max(n, 1) * (labels.numel() // labels.shape[0]))
+    t = (p * f).sum(1, keepdim=True)
+    et = (p * f * (ep + 8 * U)).sum(1, keepdim=True) + 2.0 ** -125
+    least = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    c = abs(coef) * K / max(n, 1)
+    loss, dS = ref.balance(S, labels, counts, n, scale, coef)
+    e = c * scale * (p * ((ep + 8 * U) * (f + t) + et) + 2.0 ** -125 * (f + t))
+    hs = half_step(dtype)
+    return (loss, dS, c * et.sum() + 4 * U * loss.abs(),
+            hs * dS.abs() + e * (1 + hs) + least / 2 + 2.0 ** -149)
+
+
+def check_balance(fk, S, lab, scale=1.0, coef=1.0):
+    N, K = S.shape
+    counts, rows = (torch.empty(k, dtype=torch.int32, device="cuda") for k in (K, 1))
+    fk.fk_balance_counts(lab, counts, rows)
+    loss, dS = torch.empty(1, device="cuda"), torch.full_like(S, 9.0)
+    fk.fk_balance_loss(S, lab, counts, rows, loss, dS, fk.balance_workspace(N, K, S.dtype), scale,
+                       coef)
+    wl, wd, tl, td = balance_difference_tols(S, lab, counts, int(rows), scale, coef, S.dtype)
+    within(loss, wl.reshape(1), tl, "loss")
+    within(dS, wd, td, "dS")
+
+
+BIG_K = [16, 64, 300, 1000, 4096, 4097, 8192, 9000]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", BIG_K)
+def test_balance_rows_of_one_large_score(fk, K, dtype):
+    """Rows of one value, whatever its size: p = 1 / K.  Also with one score far above."""
+    values = [v for b in (1e3, 1e4, 1e5, 1e9, 1e10, 1e12, 1e20, 1e30, 3e38) for v in (b, -b)]
+    S = torch.tensor(values, device="cuda").reshape(-1, 1).expand(-1, K)
+    lab = make_labels(len(values), K, 2, 3, 0.0)
+    check_balance(fk, S.to(TYPES[dtype]).contiguous(), lab)
+    S = rnd((len(values), K), TYPES[dtype], 4, 2.0)
+    S[:, K // 3] = torch.tensor(values, device="cuda").abs().to(TYPES[dtype])
+    check_balance(fk, S, lab)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", BIG_K)
+def test_balance_of_rows_masked_by_large_scores(fk, K, dtype):
+    """All cells but one to sixteen are masked by a large negative score; the masked row that
+    keeps none is even."""
+    t = TYPES[dtype]
+    for mask in (-1e3, -1e4, -1e9, -1e10, -1e12, -1e30, -3e38):
+        S = torch.full((20, K), mask, device="cuda").to(t)
+        real = rnd((20, K), t, 6, 2.0)
+        for i in range(1, 20):
+            at = torch.arange(min(i, 16), device="cuda") * (K // min(i, 16)) + i % 7 % (K // 16)
+            S[i, at] = real[i, at]
+        check_balance(fk, S, make_labels(20, K, 3, 5, 0.1))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", BIG_K)
+def test_balance_of_shifted_scores(fk, K, dtype):
+    """A common offset of a row's scores, as that of |c|^2 / 2: the bounds do not grow with it."""
+    for shift in (0.0, -400.0, 1e3, -1e4, 1e5, -1e6):
+        S = rnd((50, K), torch.float32, 7, 2.0)
+        S = (S + shift * torch.linspace(0.5, 1, 50, device="cuda")[:, None]).to(TYPES[dtype])
+        check_balance(fk, S, make_labels(50, K, 1, 8, 0.1), 0.7, -3.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", BIG_K)
+def test_balance_with_a_large_or_small_scale(fk, K, dtype):
+    lab = make_labels(50, K, 2, 9, 0.1)
+    for scale, size in ((2.0 ** 30, 10.0), (2.0 ** 10, 1e6), (2.0 ** 100, 1e-25), (2.0 ** -40, 1e13),
+                        (2.0 ** -100, 1e30)):
+        check_balance(fk, rnd((50, K), TYPES[dtype], 10, size), lab, scale, 2.0 ** -20)
+
+
 # ------------------------------------------------------------- together, streams, graphs
 
 def head_pass(fk, p, bufs, ws, stream=None):
