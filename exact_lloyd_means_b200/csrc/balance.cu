@@ -120,7 +120,8 @@ struct LossArgs {
     double *part;
 };
 
-// n, 1 / (n top) and coef scale K / n; and the least count.  A share f_k is worked with as its
+// n, 1 / (n top) and coef scale K / n (at most 1e38, so that the gradients of rows without
+// probabilities are 0 times a number); and the least count.  A share f_k is worked with as its
 // distance from the least one, (counts_k - least) / (n top), exact before its one rounding:
 // f_j - t_i is then formed from numbers no larger than f_j and t_i, and is 0 where all counts
 // are the same.  t_i is the weighted mean of these plus the least share, as p sums to 1.
@@ -132,7 +133,7 @@ struct LossScales {
         const int32_t r = *a.rows;
         n = static_cast<float>(r > 0 ? r : 1);
         unit = 1.f / (n * static_cast<float>(a.top));
-        gc = a.coef * a.scale * static_cast<float>(a.K) / n;
+        gc = static_cast<float>(static_cast<double>(a.coef) * a.scale * a.K / n);
         least = 0x7fffffff;
         for (int64_t k = threadIdx.x; k < a.K; k += kThreads) least = min(least, a.counts[k]);
         least = __reduce_min_sync(0xffffffffu, least);

@@ -259,7 +259,8 @@ FK_API fk_status fk_balance_loss(const void *S, fk_dtype dtype, int64_t N, int K
     if (!rows_ok(N, K) || top < 1 || N * top >= (int64_t(1) << 31)) return FK_ERR_INVALID_ARG;
     fk_status s = check_dtype(dtype);
     if (s != FK_OK) return s;
-    if (!(scale > 0.f && scale <= 1e37f) || !std::isfinite(coef))
+    if (!(scale > 0.f && scale <= 1e37f) || !std::isfinite(coef) ||
+        std::fabs(static_cast<double>(coef)) * scale * K > 1e38)
         return FK_ERR_INVALID_ARG;
     if (!counts || !rows || !loss || (N > 0 && (!S || !labels))) return FK_ERR_INVALID_ARG;
     const size_t e = elem(dtype), x = e * N * K;

@@ -490,7 +490,7 @@ FK_API fk_status fk_balance_workspace_size(int64_t N, int K, fk_dtype dtype, siz
  *   *loss = coef K sum_k f_k (sum_i p_ik / n)         (1 for an even selection, coef 1)
  *   dS_ij = coef scale (K / n) p_ij (f_j - sum_k f_k p_ik)     (N x K, optional, may be S)
  * Padding rows' scores are not used and their gradients are 0; a score of -inf has p = 0, and
- * so has every score of a row of -inf.  0 < scale <= 1e37.  counts and rows (device) come from
+ * so has every score of a row of -inf.  0 < scale <= 1e37 and |coef| scale K <= 1e38.  counts and rows (device) come from
  * fk_balance_counts; labels only tell which rows are padding.  With counts and rows of all
  * shards, the shards' losses add up to the whole. */
 FK_API fk_status fk_balance_loss(const void *S, fk_dtype dtype, int64_t N, int K,

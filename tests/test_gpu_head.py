@@ -519,7 +519,7 @@ def balance_difference_tols(S, labels, counts, n, scale, coef, dtype):
     as the shares add up to at most 1, from t.  An output is rounded to a multiple of its type's
     least subnormal, and two of its factors to one of fp32's."""
     K = S.shape[1]
-    kept = ref._kept(labels, K)[2][:, None]
+    kept = (ref._kept(labels, K)[2] & (S > -math.inf).any(1))[:, None]  # rows that have any p
     x = torch.where(kept, scale * S.double(), torch.zeros((), dtype=torch.float64, device="cuda"))
     x = x - x.max(1, keepdim=True).values
     p = torch.softmax(x, 1) * kept
@@ -597,6 +597,29 @@ def test_balance_with_a_large_or_small_scale(fk, K, dtype):
     for scale, size in ((2.0 ** 30, 10.0), (2.0 ** 10, 1e6), (2.0 ** 100, 1e-25), (2.0 ** -40, 1e13),
                         (2.0 ** -100, 1e30)):
         check_balance(fk, rnd((50, K), TYPES[dtype], 10, size), lab, scale, 2.0 ** -20)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [5, 64, 4096, 9000])
+def test_balance_at_the_largest_gradients(fk, K, dtype):
+    """coef scale K just below its limit: padding rows and rows of -inf still get zeros."""
+    t = TYPES[dtype]
+    S = rnd((12, K), t, 11, 2.0)
+    S[3] = float("-inf")
+    lab = make_labels(12, K, 1, 12, 0.0)
+    lab[5] = -1
+    scale = 2.0 ** 100
+    for coef in (9.9e37 / scale / K, -9.9e37 / scale / K):
+        check_balance(fk, S, lab, scale, coef)
+        counts, rows = (torch.empty(k, dtype=torch.int32, device="cuda") for k in (K, 1))
+        fk.fk_balance_counts(lab, counts, rows)
+        loss, dS = torch.empty(1, device="cuda"), torch.full_like(S, 9.0)
+        ws = fk.balance_workspace(12, K, t)
+        fk.fk_balance_loss(S, lab, counts, rows, loss, dS, ws, scale, coef)
+        assert torch.all(dS[3] == 0) and torch.all(dS[5] == 0) and bool(loss.isfinite())
+    with pytest.raises(fk.FkError) as e:
+        fk.fk_balance_loss(S, lab, counts, rows, loss, dS, ws, scale, 1.01e38 / scale / K)
+    assert e.value.status == fk.FK_ERR_INVALID_ARG
 
 
 # ------------------------------------------------------------- together, streams, graphs

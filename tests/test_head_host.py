@@ -137,6 +137,16 @@ def test_balance_refusals(fk):
         assert loss(**bad) == fk.FK_ERR_WORKSPACE, bad
 
 
+def test_balance_refuses_gradients_past_fp32(fk):
+    """coef scale K / n has to be a number, as padding rows multiply it by 0."""
+    order = "S dtype N K labels top counts rows scale coef loss dS ws ws_bytes stream".split()
+    ok = dict(S=_at(0), dtype=0, N=10, K=5, labels=_at(1), top=2, counts=_at(2), rows=_at(3),
+              scale=1.0, coef=1.0, loss=_at(4), dS=_at(5), ws=_at(6), ws_bytes=BIG, stream=None)
+    for bad in (dict(scale=1e37, coef=2.5), dict(scale=1e37, coef=-2.5), dict(coef=3e38),
+                dict(scale=1e37, K=64), dict(scale=1e30, coef=1e30), dict(coef=-1e35, K=1 << 20)):
+        assert _call(fk._lib.fk_balance_loss, order, ok, **bad) == fk.FK_ERR_INVALID_ARG, bad
+
+
 def test_workspace_sizes(fk):
     for name, args in (("linear_workspace", (10, 7, 5)), ("linear_backward_workspace", (10, 7, 5)),
                        ("layer_norm_backward_workspace", (10, 7)),
