@@ -459,34 +459,56 @@ GemmOperand operand(StageJobs &jobs, const void *src, int64_t rows, int cols, bo
     return GemmOperand{space, s.ld, mn_major};
 }
 
-// Products in one launch on the tensor cores, or (bf16 operands off 16-byte boundaries) each
-// without them.
-bool on_tensor_cores(const GemmArgs *args, int n) {
-    bool on = true;
-    for (int i = 0; i < n; ++i)
-        on = on && aligned(args[i].A.base, 16) && aligned(args[i].B.base, 16);
-    return on;
+// Products in one launch on the tensor cores; each whose bf16 operands lie off 16-byte boundaries
+// without them.  Either way a product's bits are its own: they do not depend on the other.
+bool on_tensor_cores(const GemmArgs &a) { return aligned(a.A.base, 16) && aligned(a.B.base, 16); }
+cudaError_t unaligned_product(const GemmArgs &a, cudaStream_t st) {
+    Epilogue ep{};
+    ep.bias = a.bias;
+    ep.R = a.R;
+    ep.C = a.C;
+    ep.Z = a.Z;
+    ep.cols = a.cols;
+    ep.act = a.act;
+    const int64_t tiles = ceil_div(a.rows, 64) * ceil_div(a.cols, 64);
+    if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = launch_pdl(
+        unaligned_kernel, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, st, a.A.base,
+        a.A.mn_major ? 1 : a.A.ld, a.A.mn_major ? a.A.ld : 1, a.B.base, a.B.mn_major ? 1 : a.B.ld,
+        a.B.mn_major ? a.B.ld : 1, a.rows, a.depth, ep);
+    if (e == cudaSuccess) note_launch();
+    return e;
 }
-cudaError_t products(const GemmArgs *args, const GemmPlan *plans, int n, const ColSums &sums,
+// `sums` are finished by the launch that joins cut products, where there is one, or else by one of
+// their own.
+cudaError_t products(const GemmArgs *args, const GemmPlan *plans, int n, ColSums sums,
                      cudaStream_t st) {
-    if (on_tensor_cores(args, n)) return launch_gemm(args, plans, n, sums, st);
+    GemmArgs on[kMaxProducts];
+    GemmPlan plan[kMaxProducts];
+    int count = 0;
+    bool cut = false;
     for (int i = 0; i < n; ++i) {
-        const GemmArgs &a = args[i];
-        Epilogue ep{};
-        ep.bias = a.bias;
-        ep.R = a.R;
-        ep.C = a.C;
-        ep.Z = a.Z;
-        ep.cols = a.cols;
-        ep.act = a.act;
-        const int64_t tiles = ceil_div(a.rows, 64) * ceil_div(a.cols, 64);
-        if (tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
-        const cudaError_t e = launch_pdl(
-            unaligned_kernel, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, st, a.A.base,
-            a.A.mn_major ? 1 : a.A.ld, a.A.mn_major ? a.A.ld : 1, a.B.base,
-            a.B.mn_major ? 1 : a.B.ld, a.B.mn_major ? a.B.ld : 1, a.rows, a.depth, ep);
+        if (!on_tensor_cores(args[i])) continue;
+        on[count] = args[i];
+        plan[count++] = plans[i];
+        cut = cut || plans[i].splits > 1;
+    }
+    if (sums.db != nullptr && !(cut && sums.parts <= kJoinParts)) {
+        const cudaError_t e = launch_pdl(col_join_kernel,
+                                         dim3(static_cast<unsigned>(ceil_div(sums.cols, 32))),
+                                         dim3(1024), 0, st, sums);
         if (e != cudaSuccess) return e;
         note_launch();
+        sums.db = nullptr;
+    }
+    if (count > 0) {
+        const cudaError_t e = launch_gemm(on, plan, count, sums, st);
+        if (e != cudaSuccess) return e;
+    }
+    for (int i = 0; i < n; ++i) {
+        if (on_tensor_cores(args[i])) continue;
+        const cudaError_t e = unaligned_product(args[i], st);
+        if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
@@ -577,16 +599,7 @@ cudaError_t linear_backward_t(const LinearArgs &a, void *ws, cudaStream_t st) {
     if (a.dX) add(G, W, a.N, a.m, a.dX, 0, L.part);
     G.mn_major = true;
     if (a.dW) add(G, X, a.m, a.N, a.dW, 1, L.part2);
-    bool cut = false;
-    for (int i = 0; i < n; ++i) cut = cut || plans[i].splits > 1;
-    if (sums.db != nullptr && !(cut && sums.parts <= kJoinParts && on_tensor_cores(args, n))) {
-        e = launch_pdl(col_join_kernel, dim3(static_cast<unsigned>(ceil_div(a.m, 32))), dim3(1024),
-                       0, st, sums);
-        if (e != cudaSuccess) return e;
-        note_launch();
-        sums.db = nullptr;
-    }
-    return n > 0 ? products(args, plans, n, sums, st) : cudaSuccess;
+    return products(args, plans, n, sums, st);
 }
 
 }  // namespace

@@ -830,6 +830,46 @@ def test_unaligned_views_give_the_aligned_bits(fk, d, m, dtype):
                      * (c.abs() + c.abs().max())).all()), i
 
 
+@pytest.mark.parametrize("N,d,m", [(300, 136, 200), (5000, 64, 72), (70, 65, 33)])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("which", ["X", "W", "dY", "Z", "X W"])
+def test_linear_backward_with_some_operands_unaligned(fk, N, d, m, act, which):
+    """A bf16 operand off 16 bytes changes only the products that read it; each output alone has
+    the bits that it has with the others."""
+    t = torch.bfloat16
+    ts = {"X": rnd((N, d), t, 1), "W": rnd((m, d), t, 2, d ** -0.5), "dY": rnd((N, m), t, 5),
+          "Z": rnd((N, m), t, 6)}
+    if act == "none":
+        ts["Z"] = None
+    ws = fk.linear_backward_workspace(N, d, m, t)
+
+    def grads(q, names):
+        o = {"dX": torch.empty((N, d), dtype=t, device="cuda"),
+             "dW": torch.empty((m, d), dtype=t, device="cuda"),
+             "dbias": torch.empty(m, device="cuda")}
+        o = {k: o[k].fill_(float("nan")) for k in names}
+        fk.fk_linear_backward(q["dY"], q["X"], q["W"], ws, act=act, Z=q["Z"], **o)
+        return o
+
+    names = ("dX", "dW", "dbias")
+    aligned = grads(ts, names)
+    q = dict(ts)
+    for k in which.split():
+        if q[k] is not None:
+            buf = torch.empty(q[k].numel() + 1, dtype=t, device="cuda")
+            q[k] = buf[1:].view(q[k].shape).copy_(ts[k])
+    got = grads(q, names)
+    want, tol = linear_backward_tols(ts["dY"], ts["X"], ts["W"], act, ts["Z"], t)
+    for name, a, b in zip(names, want, tol):
+        within(got[name], a, b, name)
+        assert torch.equal(grads(q, [name])[name], got[name]), name
+    # what each product reads as it lies: dX dY and W, dW dY and X (dY not where it is staged)
+    staged = act != "none" or m % 8 != 0
+    for name, reads in (("dX", "W"), ("dW", "X"), ("dbias", "-")):
+        if reads not in which.split() and (staged or which != "dY" or name == "dbias"):
+            assert torch.equal(got[name], aligned[name]), name
+
+
 def test_calls_on_two_streams_at_once(fk):
     """Two chains of calls that overlap on the GPU, each with a workspace of its own."""
     chains = [head_setup(fk, 3000, 256, 512, 64, seed=s) for s in (0, 50)]
