@@ -40,9 +40,13 @@ constexpr int kBandRows = 8;  // tiles of one column band that run side by side
 
 // The tensor cores cut what they add to an accumulator (about 2^-24 of the sum a step of 16,
 // always towards zero: 4.4e-6 of the result at a depth of 4096).  So fp32 products are
-// accumulated in runs of 256 of the depth, 2e-7 each, and the runs added to fp32 registers;
-// bf16 ones, whose result is rounded to 2^-9 anyway, up to 131,072 of the depth.
+// accumulated in runs of 256 of the depth, 2e-7 each, and the runs added to fp32 registers; and
+// the chain of those additions, whose roundings grow with its length (1e-6 of a sum of positive
+// terms at a depth of 2^20), is ended every 65,536: deeper products are cut into parts, which
+// are joined in order.  bf16 ones, whose result is rounded to 2^-9 anyway, take up to 131,072 of
+// the depth in one accumulation.
 constexpr int kRunChunks = 4;
+constexpr int kMaxF32Chunks = 1024;
 constexpr int kMaxBf16Chunks = 2048;
 // Parts of a tile's depth that its join adds up one after the other: with up to 148 the gradients
 // of 65536 x 64 x 64 bf16 took 53 us for 35.
@@ -584,8 +588,9 @@ __global__ void __launch_bounds__(GemmCfg<CG, BN, kPlanes<T>, OV>::kThreads, 1)
 
 // Join the partial products of the tail tiles, in order, and apply the epilogue.  Block (x,
 // y): rows of tail tile x, those of the first product (`split0` of them) before the second's.
-// Behind all `tiles`, blocks of column sums.
-template <typename T, int V>
+// Behind all `tiles`, blocks of column sums.  MANY: some product has more parts than kMaxSplits,
+// and they are added run by run, as one after the other they would round as a long chain does.
+template <typename T, int V, bool MANY>
 __global__ void __launch_bounds__(256)
     gemm_join_kernel(const __grid_constant__ GemmJobs jobs, int split0, int tiles, int tile_rows,
                      int bn, const ColSums sums) {
@@ -613,12 +618,20 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int j = 0; j < V; ++j) z[0][j] = 0.f;
         const float *p = base + lr * bn + lc;
-#pragma unroll 4
-        for (int i = 0; i < s.splits; ++i) {
+        auto add = [&](int i, float (&sum)[V]) {
             float f[V];
             load_params<V>(p + i * size, 1, f);
 #pragma unroll
-            for (int j = 0; j < V; ++j) z[0][j] += f[j];
+            for (int j = 0; j < V; ++j) sum[j] += f[j];
+        };
+        const int head = MANY && s.splits > kMaxSplits ? kMaxSplits : s.splits;
+#pragma unroll 4
+        for (int i = 0; i < head; ++i) add(i, z[0]);
+        for (int i0 = head; MANY && i0 < s.splits; i0 += kMaxSplits) {
+            float run[V] = {};
+            for (int i = i0; i < s.splits && i < i0 + kMaxSplits; ++i) add(i, run);
+#pragma unroll
+            for (int j = 0; j < V; ++j) z[0][j] += run[j];
         }
         epilogue_pieces<T, V, true>(jobs.ep[job], o, jobs.bvec[job], z);
     }
@@ -651,6 +664,7 @@ cudaError_t launch_cfg(const GemmArgs *args, const GemmPlan *plans, int n, const
     if (e != cudaSuccess) return e;
     GemmJobs jobs{};
     int64_t joined[kMaxProducts] = {};  // tail tiles to join
+    bool many = false;
     for (int i = 0; i < n; ++i) {
         const GemmArgs &a = args[i];
         const GemmPlan &p = plans[i];
@@ -684,6 +698,7 @@ cudaError_t launch_cfg(const GemmArgs *args, const GemmPlan *plans, int n, const
         jobs.units += p.full + p.tail * p.splits;
         if (i == 0) jobs.second = jobs.units;
         joined[i] = p.splits > 1 ? p.tail : 0;
+        many = many || p.splits > kMaxSplits;
     }
     const int64_t slots = device_sm_count() / CG;
     cudaLaunchConfig_t cfg = {};
@@ -708,7 +723,8 @@ cudaError_t launch_cfg(const GemmArgs *args, const GemmPlan *plans, int n, const
         constexpr int JV = OV > kVec<T> ? kVec<T> : OV;  // 16 bytes of output a thread
         const int64_t want = ceil_div(static_cast<int64_t>(device_sm_count()) * 8, tiles);
         const int64_t most = int64_t(kBM) * CG * BN / JV / 256;
-        e = launch_pdl(gemm_join_kernel<T, JV>,
+        const auto join = many ? gemm_join_kernel<T, JV, true> : gemm_join_kernel<T, JV, false>;
+        e = launch_pdl(join,
                        dim3(static_cast<unsigned>(tiles + ceil_div(sums.db ? sums.cols : 0, 32)),
                             static_cast<unsigned>(want < most ? want : most)),
                        dim3(256), 0, st, jobs, static_cast<int>(joined[0]),
@@ -781,10 +797,11 @@ void gemm_plan(const GemmSize *sizes, int n, fk_dtype dtype, GemmPlan *plans) {
                 return t;
             };
             GemmPlan p{c.cg, c.bn, 1, tiles / slots * slots, tiles % slots};
-            if (dtype == FK_BF16 && nkc > kMaxBf16Chunks) {  // every tile's depth in parts
+            const int deepest = dtype == FK_F32 ? kMaxF32Chunks : kMaxBf16Chunks;
+            if (nkc > deepest) {  // every tile's depth in parts
                 p.full = 0;
                 p.tail = tiles;
-                p.splits = static_cast<int>(ceil_div(nkc, kMaxBf16Chunks));
+                p.splits = static_cast<int>(ceil_div(nkc, deepest));
             }
             const int least = p.splits, most = least > kMaxSplits ? least : kMaxSplits;
             double best = -1;

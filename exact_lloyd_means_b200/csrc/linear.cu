@@ -252,7 +252,9 @@ cudaError_t launch_stage(const StageJobs &jobs, cudaStream_t st) {
 //   bf16, up to 4 rows: 1 x 768 x 768 1.6 / 6.2, 4 x 4096 x 4096 12.6 / 13.7; up to 8 where W
 //   has at most 2^20 elements: 8 x 768 x 768 4.1 / 6.1, but 8 x 768 x 4096 8.5 / 6.7.
 bool few_rows(int64_t N, int d, int m, fk_dtype dtype) {
-    if (dtype == FK_F32) return N <= 16;
+    // (in fp32 a thread adds up d / 128 products one after the other: up to 2^22 of them, as
+    // 2^15 additions a thread, averaged over 128 threads, round like the tensor cores' route)
+    if (dtype == FK_F32) return N <= 16 && d <= (1 << 22);
     return N <= 4 || (N <= 8 && static_cast<int64_t>(m) * d <= (1 << 20));
 }
 

@@ -455,7 +455,8 @@ FK_API fk_status fk_linear_backward_workspace_size(int64_t N, int d, int m, fk_d
  * With W = C and bias = -||c||^2 / 2 it scores points against every centroid.
  * Precision: FK_BF16 products are exact, accumulated in fp32, and the outputs rounded once.
  * FK_F32 operands are taken as three bf16 numbers each, with the six products that matter to
- * fp32; the sums are within about 2^-22 of the result at any depth.  fp32 values below about
+ * fp32; a sum is within about 2^-20 of the sum of its terms' magnitudes at any depth (of positive
+ * terms 4e-7 of it, nearly all of it downwards; with signs far less).  fp32 values below about
  * 2^-110 lose their lowest bits, and where an operand is infinite a result may be NaN instead
  * of infinite.  GELU and SiLU are within a few units of 2^-24 of |z|. */
 FK_API fk_status fk_linear(const void *X, fk_dtype dtype, int64_t N, int d, const void *W,

@@ -349,6 +349,34 @@ def test_linear_fp32_error_does_not_grow_with_the_depth(fk, depth):
     assert off(dW, want) <= 9.5e-7
 
 
+def test_linear_fp32_of_positive_terms_over_a_very_long_depth(fk):
+    """Whole tiles over 400,000 rows, where every cut and every rounding goes with the sum.  A
+    run's cuts are at most 16 2^-24 = 9.5e-7 of it and half of that on average; a chain of r
+    additions with rounding to nearest is off by 2^-24 sqrt(r) / 3 (each by u / sqrt(3) of the
+    running sum, whose mean square is a third of its end), which for the 256 runs of 65,536 rows
+    is 3.2e-7 and for all of 400,000 rows would be 7.9e-7."""
+    N, d, m = 400_000, 2048, 1280
+    X, dY = rnd((N, d), seed=1).abs_(), rnd((N, m), seed=2).abs_()
+    dW = torch.empty((m, d), device="cuda")
+    fk.fk_linear_backward(dY, X, dW.clone(), fk.linear_backward_workspace(N, d, m), dW=dW)
+    want = dY[:, :64].double().t() @ X[:, :64].double()
+    e = (dW[:64, :64].double() - want) / want
+    assert float(e.square().mean().sqrt()) <= math.hypot(4.8e-7, 3.2e-7)
+
+
+def test_linear_fp32_few_rows_of_a_very_long_depth(fk):
+    """Few rows add up in one chain a thread, of at most 2^15: 2^-24 sqrt(2^15) / 3 = 3.6e-6, over
+    128 threads 3.2e-7 on average; deeper ones go the way of many rows, whose parts of 65,536 are
+    joined in runs of 32 (1.1e-7), of which 2^25 takes 16 (0.8e-7)."""
+    for N, d in ((2, 1 << 22), (3, (1 << 22) + 8), (2, 1 << 25), (1, (1 << 25) + 1)):
+        X, W = rnd((N, d), seed=1).abs_(), rnd((5, d), seed=2).abs_()
+        Y = torch.empty((N, 5), device="cuda")
+        fk.fk_linear(X, W, Y, fk.linear_workspace(N, d, 5))
+        want = X.double() @ W.double().t()
+        e = (Y.double() - want) / want
+        assert float(e.square().mean().sqrt()) <= math.hypot(4.8e-7, 3.2e-7), d
+
+
 def test_linear_bf16_over_a_very_long_depth(fk):
     """A gradient over 300,000 rows: the depth is cut into parts, and the error stays that of
     one rounding to bf16 (2^-8 at most, a third of that on average)."""
