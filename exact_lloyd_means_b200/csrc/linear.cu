@@ -361,6 +361,9 @@ cudaError_t launch_few_rows(const LinearArgs &a, cudaStream_t st) {
 // ----------------------------------------------------------------- unaligned bf16 operands
 // C[i][j] = sum_k A(i, k) B(j, k) on the CUDA cores, for bf16 operands that start off a
 // 16-byte boundary: any strides, no staging (whose space would be as large as the operand).
+// Sums are added up in runs of kUnalignedRun and the runs apart: one chain of fp32 additions of
+// positive products of bf16 numbers is 0.3% low after 2^22 of them and 3.5% after 2^24.
+constexpr int kUnalignedRun = 4096;
 __global__ void __launch_bounds__(256)
     unaligned_kernel(const uint16_t *__restrict__ A, int64_t ar, int64_t ak,
                      const uint16_t *__restrict__ B, int64_t br, int64_t bk, int64_t rows,
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(256)
     const int64_t r0 = static_cast<int64_t>(blockIdx.x) / ct * 64;
     const int64_t c0 = static_cast<int64_t>(blockIdx.x) % ct * 64;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
+    float sum[4][4] = {}, acc[4][4] = {};
     for (int64_t k0 = 0; k0 < depth; k0 += 16) {
         for (int t = threadIdx.x; t < 1024; t += 256) {
             const int k = ak == 1 ? t & 15 : t >> 6, i = ak == 1 ? t >> 4 : t & 63;
@@ -393,13 +396,22 @@ __global__ void __launch_bounds__(256)
                 for (int j = 0; j < 4; ++j)
                     acc[i][j] += sa[k][ty + 16 * i] * sb[k][tx + 16 * j];
         __syncthreads();
+        if ((k0 + 16) % kUnalignedRun == 0 || k0 + 16 >= depth) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sum[i][j] += acc[i][j];
+                    acc[i][j] = 0.f;
+                }
+        }
     }
     for (int i = 0; i < 4; ++i)
         for (int j = 0; j < 4; ++j) {
             const int64_t r = r0 + ty + 16 * i, c = c0 + tx + 16 * j;
             if (r >= rows || c >= ep.cols) continue;
             const int64_t o = r * ep.cols + c;
-            const float z = acc[i][j] + (ep.bias ? ep.bias[c] : 0.f);
+            const float z = sum[i][j] + (ep.bias ? ep.bias[c] : 0.f);
             const float res = ep.R ? bf16_val(static_cast<const uint16_t *>(ep.R)[o]) : 0.f;
             if (ep.Z) static_cast<uint16_t *>(ep.Z)[o] = bf16_bits(z);
             static_cast<uint16_t *>(ep.C)[o] = bf16_bits(act_value(z, ep.act) + res);

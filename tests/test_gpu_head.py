@@ -898,6 +898,20 @@ def test_linear_backward_with_some_operands_unaligned(fk, N, d, m, act, which):
             assert torch.equal(got[name], aligned[name]), name
 
 
+def test_linear_backward_of_unaligned_operands_over_very_many_rows(fk):
+    """Positive terms over 2^23 rows: fp32 sums round to bf16 once, whatever the route."""
+    t, N = torch.bfloat16, 1 << 23
+    buf = torch.empty(2, N * 8 + 1, dtype=t, device="cuda")
+    X, dY = buf[0, 1:].view(N, 8), buf[1, :-1].view(N, 8)
+    X.copy_(rnd((N, 8), seed=1).abs_())
+    dY.copy_(rnd((N, 8), seed=2).abs_())
+    dW = torch.empty((8, 8), dtype=t, device="cuda")
+    fk.fk_linear_backward(dY, X, dW.clone(), fk.linear_backward_workspace(N, 8, 8, t), dW=dW)
+    want = dY.double().t() @ X.double()
+    # a run of 4096 and 2048 runs: (2^-24 / 3)(sqrt(4096) + sqrt(2048)) = 2.2e-6, next to 2^-8
+    assert float(((dW.double() - want).abs() / want).max()) <= half_step(t) + 1e-5
+
+
 def test_calls_on_two_streams_at_once(fk):
     """Two chains of calls that overlap on the GPU, each with a workspace of its own."""
     chains = [head_setup(fk, 3000, 256, 512, 64, seed=s) for s in (0, 50)]
