@@ -252,13 +252,17 @@ cudaError_t launch_stage(const StageJobs &jobs, cudaStream_t st) {
 //   bf16, up to 4 rows: 1 x 768 x 768 1.6 / 6.2, 4 x 4096 x 4096 12.6 / 13.7; up to 8 where W
 //   has at most 2^20 elements: 8 x 768 x 768 4.1 / 6.1, but 8 x 768 x 4096 8.5 / 6.7.
 bool few_rows(int64_t N, int d, int m, fk_dtype dtype) {
-    // (in fp32 a thread adds up d / 128 products one after the other: up to 2^22 of them, as
-    // 2^15 additions a thread, averaged over 128 threads, round like the tensor cores' route)
-    if (dtype == FK_F32) return N <= 16 && d <= (1 << 22);
+    if (dtype == FK_F32) return N <= 16;
     return N <= 4 || (N <= 8 && static_cast<int64_t>(m) * d <= (1 << 20));
 }
 
-template <typename T, int NR, int CW>
+// Depth after which a block joins its threads' sums: a thread adds up 1/128 of it, 8192 products,
+// one after the other, and longer chains would show (fp32 sums of positive terms were 3e-7 low at
+// a depth of 2^22 in one chain a thread and 2.3e-5 at 2^25).
+constexpr int64_t kFewRun = 1 << 20;
+
+// LONG: a depth of more than kFewRun.
+template <typename T, int NR, int CW, bool LONG>
 __global__ void __launch_bounds__(128)
     few_rows_kernel(const T *__restrict__ X, const T *__restrict__ W, int N, int d, int vec,
                     const Epilogue ep) {
@@ -295,29 +299,48 @@ __global__ void __launch_bounds__(128)
             }
         }
     };
-    if (vec) {
+    // the threads' sums over columns k0 .. k1 - 1, joined: thread r * CW + c has that of (r, c)
+    auto run = [&](int64_t k0, int64_t k1) {
+        if (vec) {
 #pragma unroll 2
-        for (int64_t k = threadIdx.x * V; k < d; k += 128 * V)
-            step(k, std::integral_constant<int, V>{});
-    } else {
+            for (int64_t k = k0 + threadIdx.x * V; k < k1; k += 128 * V)
+                step(k, std::integral_constant<int, V>{});
+        } else {
 #pragma unroll 2
-        for (int64_t k = threadIdx.x; k < d; k += 128) step(k, std::integral_constant<int, 1>{});
-    }
-#pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-        for (int c = 0; c < CW; ++c) {
-            if (r < N) s[r][c] = warp_sum_f(s[r][c]);
-            if (lane == 0) red[warp][r * CW + c] = s[r][c];
+            for (int64_t k = k0 + threadIdx.x; k < k1; k += 128)
+                step(k, std::integral_constant<int, 1>{});
         }
-    __syncthreads();
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int c = 0; c < CW; ++c) {
+                if (r < N) s[r][c] = warp_sum_f(s[r][c]);
+                if (lane == 0) red[warp][r * CW + c] = s[r][c];
+            }
+        __syncthreads();
+        float v = 0.f;
+        if (static_cast<int>(threadIdx.x) < NR * CW) {
+            v = red[0][threadIdx.x];
+#pragma unroll
+            for (int t = 1; t < 4; ++t) v += red[t][threadIdx.x];
+        }
+        return v;
+    };
+    float z = run(0, LONG ? kFewRun : d);
+    if constexpr (LONG) {
+        for (int64_t k0 = kFewRun; k0 < d; k0 += kFewRun) {
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int c = 0; c < CW; ++c) s[r][c] = 0.f;
+            z += run(k0, k0 + kFewRun < d ? k0 + kFewRun : d);
+        }
+    }
     if (static_cast<int>(threadIdx.x) >= NR * CW) return;
     const int r = threadIdx.x / CW;
     const int64_t col = c0 + threadIdx.x % CW;
     if (r >= N || col >= ep.cols) return;
-    float z = red[0][threadIdx.x];
-#pragma unroll
-    for (int t = 1; t < 4; ++t) z += red[t][threadIdx.x];
     z = __fadd_rn(z, ep.bias != nullptr ? ep.bias[col] : 0.f);
     const int64_t o = r * ep.cols + col;
     const float res = ep.R != nullptr ? head_load(static_cast<const T *>(ep.R) + o) : 0.f;
@@ -346,16 +369,19 @@ cudaError_t launch_few_rows(const LinearArgs &a, cudaStream_t st) {
     };
     // four columns a block from 1024 on (4 x 768 x 4096 bf16 5.3 against 6.3 with one), one
     // where the GPU would stay empty (8 x 4096 x 100 bf16 4.1 against 9.2)
-    auto rows = [&](auto columns) {
+    auto rows = [&](auto columns, auto deep) {
         constexpr int CW = decltype(columns)::value;
-        if (N == 1) return launch(few_rows_kernel<T, 1, CW>, CW);
-        if (N <= 2) return launch(few_rows_kernel<T, 2, CW>, CW);
-        if (N <= 4) return launch(few_rows_kernel<T, 4, CW>, CW);
-        if (N <= 8 || sizeof(T) == 2) return launch(few_rows_kernel<T, 8, CW>, CW);
-        return launch(few_rows_kernel<T, sizeof(T) == 4 ? 16 : 8, CW>, CW);
+        constexpr bool L = decltype(deep)::value;
+        if (N == 1) return launch(few_rows_kernel<T, 1, CW, L>, CW);
+        if (N <= 2) return launch(few_rows_kernel<T, 2, CW, L>, CW);
+        if (N <= 4) return launch(few_rows_kernel<T, 4, CW, L>, CW);
+        if (N <= 8 || sizeof(T) == 2) return launch(few_rows_kernel<T, 8, CW, L>, CW);
+        return launch(few_rows_kernel<T, sizeof(T) == 4 ? 16 : 8, CW, L>, CW);
     };
-    return a.m >= 1024 ? rows(std::integral_constant<int, 4>{})
-                       : rows(std::integral_constant<int, 1>{});
+    using One = std::integral_constant<int, 1>;
+    if (a.d > kFewRun) return rows(One{}, std::true_type{});
+    return a.m >= 1024 ? rows(std::integral_constant<int, 4>{}, std::false_type{})
+                       : rows(One{}, std::false_type{});
 }
 
 // ----------------------------------------------------------------- unaligned bf16 operands

@@ -365,10 +365,9 @@ def test_linear_fp32_of_positive_terms_over_a_very_long_depth(fk):
 
 
 def test_linear_fp32_few_rows_of_a_very_long_depth(fk):
-    """Few rows add up in one chain a thread, of at most 2^15: 2^-24 sqrt(2^15) / 3 = 3.6e-6, over
-    128 threads 3.2e-7 on average; deeper ones go the way of many rows, whose parts of 65,536 are
-    joined in runs of 32 (1.1e-7), of which 2^25 takes 16 (0.8e-7)."""
-    for N, d in ((2, 1 << 22), (3, (1 << 22) + 8), (2, 1 << 25), (1, (1 << 25) + 1)):
+    """Few rows add up in chains of at most 2^13 a thread: 2^-24 sqrt(2^13) / 3 = 1.8e-6, over 128
+    threads 1.6e-7; runs of 2^20 are joined one after the other (of 32: 1.1e-7)."""
+    for N, d in ((2, 1 << 20), (1, (1 << 20) + 4), (16, (1 << 20) + 3), (2, 1 << 22), (3, (1 << 22) + 8), (2, 1 << 25), (1, (1 << 25) + 1)):
         X, W = rnd((N, d), seed=1).abs_(), rnd((5, d), seed=2).abs_()
         Y = torch.empty((N, 5), device="cuda")
         fk.fk_linear(X, W, Y, fk.linear_workspace(N, d, 5))
@@ -910,6 +909,19 @@ def test_linear_backward_of_unaligned_operands_over_very_many_rows(fk):
     want = dY.double().t() @ X.double()
     # a run of 4096 and 2048 runs: (2^-24 / 3)(sqrt(4096) + sqrt(2048)) = 2.2e-6, next to 2^-8
     assert float(((dW.double() - want).abs() / want).max()) <= half_step(t) + 1e-5
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_few_rows_over_a_very_long_depth(fk, dtype):
+    t = TYPES[dtype]
+    for d in (1 << 20, (1 << 20) + 8, (1 << 20) + 9, (1 << 22) + 1032):
+        X, W, b = rnd((2, d), t, 1), rnd((3, d), t, 2, d ** -0.5), rnd((3,), seed=3)
+        Y = torch.empty((2, 3), dtype=t, device="cuda")
+        fk.fk_linear(X, W, Y, fk.linear_workspace(2, d, 3, t), bias=b)
+        want = X.double() @ W.double().t() + b.double()
+        # sums of terms with signs: 2^-20 of their magnitudes, 0.64 sqrt(d)
+        tol = half_step(t) * want.abs() + 2.0 ** -20 * (0.64 * d ** 0.5 + b.abs().double())
+        within(Y, want, tol, d)
 
 
 def test_calls_on_two_streams_at_once(fk):
