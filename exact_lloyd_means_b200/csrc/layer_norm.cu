@@ -411,7 +411,9 @@ __global__ void __launch_bounds__(kThreads)
             phase ^= 1u;
         }
         if (dX != nullptr && row) {
-            // (as the formula has it: r w - r mean(w) would not be 0 where w is its mean)
+            // (as the formula has it: r w - r mean(w) would round r w first.  Where all w of a
+            // row are the same, w - mean(w) is what the mean's sum and its division by d round: 0
+            // for d a power of two, a few units of 2^-24 |w| otherwise)
             const float na = -a * inv, nb = -b * inv;
             const F2 na2 = f2(na, na), nb2 = f2(nb, nb);
             T *o = dX + i * d + t * V;

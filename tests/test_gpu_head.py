@@ -179,6 +179,32 @@ def test_layer_norm_backward_of_rows_without_a_gradient(fk, d, dtype):
         assert torch.all(dX == 0)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [3, 40, 129, 768, 1000, 1024, 5001, 9000])
+def test_layer_norm_of_constant_rows(fk, d, dtype):
+    """Rows of one value, in both directions.  A mean of d equal values is off by the roundings of
+    its sum (d / 16 additions and 24 more) and of 1 / d: n u of the value.  Forward, x - mean is that
+    and rstd at most 1 / sqrt(eps); backward, w - mean(w) is that, and h, formed from a mean that is
+    the value itself, is 0."""
+    t = TYPES[dtype]
+    n = d / 16 + 24
+    X = rnd((70, 1), t, 1, shift=0.5).expand(70, d).contiguous()
+    Y, mean, rstd = torch.empty_like(X), *(torch.empty(70, device="cuda") for _ in range(2))
+    fk.fk_layer_norm(X, None, None, Y, 1e-5, mean, rstd)
+    x = X[:, :1].double()
+    assert bool((Y.double().abs() <= 1.01 * n * U * x.abs() * 1e-5 ** -0.5).all())
+    assert bool(((mean.double() - x[:, 0]).abs() <= n * U * x[:, 0].abs()).all())
+    dY = rnd((70, 1), t, 2).expand(70, d).contiguous()
+    gamma = torch.full((d,), 0.7, device="cuda")
+    mean, rstd = X[:, 0].float().contiguous(), torch.full((70,), 1e-5 ** -0.5, device="cuda")
+    for g in (None, gamma):
+        dX = torch.full_like(X, float("nan"))
+        fk.fk_layer_norm_backward(dY, X, g, mean, rstd, dX, None, None,
+                                  fk.layer_norm_backward_workspace(70, d, t))
+        w = dY[:, :1].double().abs() * (1.0 if g is None else 0.7)
+        assert bool((dX.double().abs() <= 1.01 * (n + 4) * U * w * 1e-5 ** -0.5).all())
+
+
 @pytest.mark.parametrize("N,d", [(2003, 1000), (1501, 1024), (1201, 1800), (900, 2048)])
 def test_layer_norm_backward_of_wide_fp32_rows(fk, N, d):
     test_layer_norm_backward(fk, N, d, "f32")
