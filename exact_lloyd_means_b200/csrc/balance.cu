@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     double total = 0.0;
     int slot = 0, stage = 0;
     uint32_t phase = 0;
+    bool ok = true;
     int64_t i = first + grp;
     // the first selection of the next row, read a turn ahead (the others only if it is none)
     int32_t next = i < a.N ? a.labels[i * a.top] : -1;
@@ -323,8 +324,10 @@ __global__ void __launch_bounds__(kThreads, 3)
         const int32_t lab = next;
         if (i + step < a.N) next = a.labels[(i + step) * a.top];
         const bool on = i < a.N && ((lab >= 0 && lab < a.K) || (a.top > 1 && row_selects(a, i)));
-        // a wait that runs out is recorded, and the pass runs to its end without its data
+        // a wait that runs out is recorded, and the pass runs to its end without its data; nothing
+        // more is brought then, as the slot's last copy may still be on its way
         if (!ptx::mbar_wait(&full[stage], phase, &abort_flag, wait_ns)) {
+            ok = false;
             *const_cast<volatile uint32_t *>(&abort_flag) = 1u;
             err[0] = kErrTimeout;
         }
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         if constexpr (TPR <= 32) __syncthreads();
         slot ^= 1;
         // every thread has the slot's rows in registers now
-        if (threadIdx.x == 0) bring(i0 + stages * step, stage);
+        if (threadIdx.x == 0 && ok) bring(i0 + stages * step, stage);
         if (++stage == stages) {
             stage = 0;
             phase ^= 1u;

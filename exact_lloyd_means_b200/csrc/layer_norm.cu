@@ -360,6 +360,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     int slot = 0, s = 0;
     uint32_t phase = 0;
+    bool ok = true;
     for (int64_t i0 = first; i0 < N; i0 += step) {
         const int64_t i = i0 + grp;
         const bool row = i < N;
@@ -368,8 +369,10 @@ __global__ void __launch_bounds__(kThreads)
             mu1 = mean[i + step];
             r1 = rstd[i + step];
         }
-        // a wait that runs out is recorded, and the pass runs to its end without its data
+        // a wait that runs out is recorded, and the pass runs to its end without its data; nothing
+        // more is brought then, as the slot's last copy may still be on its way
         if (!ptx::mbar_wait(&full[s], phase, &abort_flag, wait_ns)) {
+            ok = false;
             *const_cast<volatile uint32_t *>(&abort_flag) = 1u;
             err[0] = kErrTimeout;
         }
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kThreads)
         if constexpr (TPR <= 32) __syncthreads();
         slot ^= 1;
         // every thread has the slot's rows in registers now
-        if (threadIdx.x == 0) bring(i0 + stages * step, s);
+        if (threadIdx.x == 0 && ok) bring(i0 + stages * step, s);
         if (++s == stages) {
             s = 0;
             phase ^= 1u;
