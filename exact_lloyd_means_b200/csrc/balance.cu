@@ -179,7 +179,8 @@ __device__ __forceinline__ float soft_base(float m) { return m == -INFINITY ? 0.
 template <int W>
 __device__ __forceinline__ float lanes_max(float m) {
     if constexpr (W == 32) {
-        asm("redux.sync.max.NaN.f32 %0, %0, 0xffffffff;" : "+f"(m));
+        // (volatile: a meeting of the warp's lanes must stay where it stands)
+        asm volatile("redux.sync.max.NaN.f32 %0, %0, 0xffffffff;" : "+f"(m));
     } else {
 #pragma unroll
         for (int o = W / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
