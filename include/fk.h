@@ -406,7 +406,8 @@ FK_API fk_status fk_ivf_search(const float *Q, int64_t nq, int d, const float *C
  *     pointers (16-byte aligned rows are faster, for bf16 products by far); N = 0 writes no
  *     row, and gradients that are sums over rows become 0;
  *   - products, statistics and sums are accumulated in fp32 or more and every output is
- *     rounded once; no floating-point atomics, so results repeat bit for bit;
+ *     rounded once (what is rounded before that, the operator says); no floating-point
+ *     atomics, so results repeat bit for bit;
  *   - outputs overlap neither an input nor one another, except where "may be" says so
  *     (then they start at the same address); NULL skips an optional output;
  *   - calls are asynchronous on `stream` and can be captured into a CUDA graph (each graph
@@ -415,7 +416,9 @@ FK_API fk_status fk_ivf_search(const float *Q, int64_t nq, int d, const float *C
 /* Row layer norm: mean_i and rstd_i = 1 / sqrt(var_i + eps) of row i (var over the d
  * columns, divided by d), Y = (X - mean) rstd gamma + beta.  gamma, beta: d floats or NULL
  * (1 and 0).  mean, rstd: N floats, optional (the backward pass needs them).  Y may be X.
- * eps >= 0. */
+ * eps >= 0.  mean is rounded to fp32, so h = (X - mean) rstd is off by about 2^-24 |mean| rstd
+ * in both passes; a row whose squared distances from its mean overflow fp32 (1e19 each) has
+ * rstd = 0. */
 FK_API fk_status fk_layer_norm(const void *X, fk_dtype dtype, int64_t N, int d,
                                const float *gamma, const float *beta, float eps, void *Y,
                                float *mean, float *rstd, fk_stream_t stream);
@@ -453,7 +456,8 @@ FK_API fk_status fk_linear_backward_workspace_size(int64_t N, int d, int m, fk_d
  * residual: N x m or NULL, Y: N x m (may be residual), Z: N x m, optional: the
  * pre-activation, which the backward pass needs when act is not FK_ACT_NONE.
  * With W = C and bias = -||c||^2 / 2 it scores points against every centroid.
- * Precision: FK_BF16 products are exact, accumulated in fp32, and the outputs rounded once.
+ * Precision: FK_BF16 products are exact, accumulated in fp32 (the tensor cores cut towards zero:
+ * under 2^-11 of the terms' magnitudes at any depth), and the outputs rounded once.
  * FK_F32 operands are taken as three bf16 numbers each, with the six products that matter to
  * fp32; a sum is within about 2^-20 of the sum of its terms' magnitudes at any depth (of positive
  * terms 4e-7 of it, nearly all of it downwards; with signs far less).  fp32 values below about
