@@ -724,7 +724,7 @@ def fk_balance_loss(S: torch.Tensor, labels: torch.Tensor, counts: torch.Tensor,
                     rows: torch.Tensor, loss: torch.Tensor, dS: torch.Tensor | None,
                     ws: torch.Tensor, scale: float = 1.0, coef: float = 1.0, stream=None):
     """Balance loss (fp32 [1]) of the scores S [N, K] and its gradient dS (may be S; None
-    skips it), with the counts and rows of fk_balance_counts."""
+    skips it), with the counts and rows of fk_balance_counts.  |coef| scale K is at most 1e38."""
     dev = _home(S, "S")
     N, K = shape = S.shape
     t = S.dtype
